@@ -467,6 +467,154 @@ size_t intlora_train_backward_workspace_size(const intlora_train_backward_job* j
 intlora_status intlora_train_backward_batched(const intlora_train_backward_job* jobs, int32_t count,
                                               void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------------------------------------------------
+ * Around the linears in a training step. The pages train the factors of
+ * diffusion and language models [notes, 两种实现版本; summary, "Measured
+ * effects"] and leave the rest of the step to the host framework; these calls
+ * are the parts that stand next to the linears' forward and backward above:
+ * the embedding in front of them, the layer norm whose output they take and
+ * whose input gradient continues their dX, and the clipping of the factors'
+ * gradients dA, dB by their global norm.
+ *
+ * Elements are fp32, bf16 or fp16 (INTLORA_TYPE_*), each tensor with a type of
+ * its own; arithmetic, statistics and sums are fp32 or wider and every output
+ * is rounded once, to nearest, ties to even. Matrices are row-major with a row
+ * stride ld in elements (>= n), any alignment of whole elements; rows at
+ * 16-byte boundaries with n % 8 == 0 take 16-byte accesses, others single
+ * elements. Results do not depend on the order in which blocks run.
+ * tokens, n and vocab < 2^31; every rows * ld at most 2^40.
+ * ------------------------------------------------------------------------ */
+#define INTLORA_TYPE_F32 0
+#define INTLORA_TYPE_BF16 1
+#define INTLORA_TYPE_F16 2
+
+/* Layer norm of every row: y = (x - mean) rstd weight + bias, with
+ * mean = (1/n) sum x, rstd = ((1/n) sum (x - mean)^2 + eps)^-1/2.
+ * weight, bias (both param_type, [n]) may be NULL (1 and 0); mean and rstd
+ * (fp32 [tokens], what the backward takes) may be NULL. n >= 1, eps finite and
+ * >= 0; a constant row with eps = 0 gives what 0 / 0 gives. One launch a job;
+ * the jobs of a call do not depend on one another. Asynchronous on `stream`;
+ * no workspace. */
+typedef struct intlora_layer_norm_job {
+    const void* x;            /* tokens x n */
+    const void* weight;
+    const void* bias;
+    void* y;                  /* tokens x n (overwritten) */
+    float* mean;
+    float* rstd;
+    int64_t tokens, n;
+    int64_t ld_x, ld_y;
+    int32_t x_type, param_type, y_type;
+    float eps;
+} intlora_layer_norm_job;
+
+intlora_status intlora_layer_norm_batched(const intlora_layer_norm_job* jobs, int32_t count,
+                                          void* stream);
+
+/* Its gradients. With xh = (x - mean) rstd, g = dy weight:
+ *   dx = rstd (g - (1/n) sum g - xh (1/n) sum g xh)        (per row)
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy   (fp32 [n])
+ * mean and rstd are those of the forward. dx, dweight and dbias may each be
+ * NULL (not computed). dweight and dbias are overwritten, or added to with
+ * accumulate != 0; tokens = 0 gives zero sums. Workspace (256-byte aligned):
+ * one row of partial sums per thread block, for jobs with dweight or dbias. */
+typedef struct intlora_layer_norm_backward_job {
+    const void* dy;           /* tokens x n */
+    const void* x;            /* tokens x n, the forward's input */
+    const void* weight;       /* [n] or NULL */
+    const float* mean;        /* [tokens] */
+    const float* rstd;        /* [tokens] */
+    void* dx;                 /* tokens x n */
+    float* dweight;
+    float* dbias;
+    int64_t tokens, n;
+    int64_t ld_dy, ld_x, ld_dx;
+    int32_t dy_type, x_type, param_type, dx_type;
+    int32_t accumulate;
+} intlora_layer_norm_backward_job;
+
+size_t intlora_layer_norm_backward_workspace_size(const intlora_layer_norm_backward_job* jobs,
+                                                  int32_t count);
+intlora_status intlora_layer_norm_backward_batched(const intlora_layer_norm_backward_job* jobs,
+                                                   int32_t count, void* ws, size_t ws_bytes,
+                                                   void* stream);
+
+/* Embedding lookup: y[t] = scale * table[ids[t]]. ids: int32 or int64
+ * (id_bytes 4 or 8). An id outside [0, vocab) reads nothing: its row of y is
+ * zero, and if `invalid` (a device int32, may be NULL) is given, the number of
+ * such ids is added to it. Asynchronous on `stream`; no workspace. */
+typedef struct intlora_embedding_job {
+    const void* table;        /* vocab x n */
+    const void* ids;          /* [tokens] */
+    void* y;                  /* tokens x n (overwritten) */
+    int32_t* invalid;
+    int64_t vocab, n, tokens;
+    int64_t ld_table, ld_y;
+    int32_t table_type, y_type;
+    int32_t id_bytes;
+    float scale;
+} intlora_embedding_job;
+
+intlora_status intlora_embedding_batched(const intlora_embedding_job* jobs, int32_t count,
+                                         void* stream);
+
+/* Its gradient: dtable[v] = scale * sum of dy[t] over the tokens with
+ * ids[t] = v. Tokens whose id is padding_id (-1: none) or lies outside
+ * [0, vocab) add nothing; the latter are counted in `invalid`. accumulate = 0:
+ * the whole of dtable is written (rows without tokens as zeros); else the sums
+ * are added to the rows that have tokens, and no other row is read or written.
+ * The tokens are sorted by id first, so a row's sum has one owner and the same
+ * bits on every run. Workspace (256-byte aligned): 16 bytes per token for the
+ * sorted lists and n fp32 per 32 tokens for partial sums of frequent ids. */
+typedef struct intlora_embedding_backward_job {
+    const void* dy;           /* tokens x n */
+    const void* ids;          /* [tokens] */
+    void* dtable;             /* vocab x n */
+    int32_t* invalid;
+    int64_t vocab, n, tokens;
+    int64_t padding_id;
+    int64_t ld_dy, ld_dtable;
+    int32_t dy_type, dtable_type;
+    int32_t id_bytes;
+    int32_t accumulate;
+    float scale;
+} intlora_embedding_backward_job;
+
+size_t intlora_embedding_backward_workspace_size(const intlora_embedding_backward_job* jobs,
+                                                 int32_t count);
+intlora_status intlora_embedding_backward_batched(const intlora_embedding_backward_job* jobs,
+                                                  int32_t count, void* ws, size_t ws_bytes,
+                                                  void* stream);
+
+/* Global norm of many gradient tensors, and clipping by it:
+ *   norm = sqrt(sum over all tensors of g^2)      (summed in fp64, stored fp32)
+ *   g <- g * min(1, max_norm / (norm + 1e-6))     (in place)
+ * The gradients are only read where the factor is 1. A NaN norm makes every
+ * gradient NaN, an infinite one makes finite gradients 0: test *norm. Tensors
+ * are dense (count elements from g on) and of any number; those that
+ * clipping writes must not overlap (checked). max_norm finite and >= 0. norm is
+ * a device float. No tensors: norm 0.
+ *
+ * intlora_grad_norm_batched only reads; intlora_grad_clip_batched scales by a
+ * norm given on the device (with layers sharded over ranks: the root of the
+ * ranks' summed squares); intlora_clip_grad_norm_batched does both, in one
+ * launch each per 512 tensors. Workspace (256-byte aligned): one fp64 partial
+ * sum per thread block. */
+typedef struct intlora_grad_job {
+    void* g;
+    int64_t count;
+    int32_t type;
+} intlora_grad_job;
+
+size_t intlora_grad_norm_workspace_size(const intlora_grad_job* jobs, int32_t count);
+intlora_status intlora_grad_norm_batched(const intlora_grad_job* jobs, int32_t count, float* norm,
+                                         void* ws, size_t ws_bytes, void* stream);
+intlora_status intlora_grad_clip_batched(const intlora_grad_job* jobs, int32_t count, float max_norm,
+                                         const float* norm, void* stream);
+intlora_status intlora_clip_grad_norm_batched(const intlora_grad_job* jobs, int32_t count,
+                                              float max_norm, float* norm, void* ws,
+                                              size_t ws_bytes, void* stream);
+
 /* Device health check: synchronizes the device, then returns
  * INTLORA_ERR_TIMEOUT (with the count in intlora_last_error()) when bounded
  * device-side waits gave up since the previous intlora_device_status() call

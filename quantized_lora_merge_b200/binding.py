@@ -23,6 +23,8 @@ _c_f32, _c_ptr, _c_size = ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
 DIST_LAPLACE, DIST_GAUSSIAN, DIST_CAUCHY, DIST_STUDENT_T2 = 0, 1, 2, 3   # INTLORA_DIST_*
 
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2             # INTLORA_TYPE_*
+
 STATUS = {0: "INTLORA_OK", 1: "INTLORA_ERR_INVALID_ARG", 2: "INTLORA_ERR_UNSUPPORTED",
           3: "INTLORA_ERR_WORKSPACE", 4: "INTLORA_ERR_CUDA", 5: "INTLORA_ERR_TIMEOUT"}
 
@@ -81,6 +83,40 @@ class intlora_int_gemm_job(ctypes.Structure):
                 ("y_bf16", _c_i32)]
 
 
+class intlora_layer_norm_job(ctypes.Structure):
+    _fields_ = [("x", _c_ptr), ("weight", _c_ptr), ("bias", _c_ptr), ("y", _c_ptr),
+                ("mean", _c_ptr), ("rstd", _c_ptr), ("tokens", _c_i64), ("n", _c_i64),
+                ("ld_x", _c_i64), ("ld_y", _c_i64), ("x_type", _c_i32), ("param_type", _c_i32),
+                ("y_type", _c_i32), ("eps", _c_f32)]
+
+
+class intlora_layer_norm_backward_job(ctypes.Structure):
+    _fields_ = [("dy", _c_ptr), ("x", _c_ptr), ("weight", _c_ptr), ("mean", _c_ptr),
+                ("rstd", _c_ptr), ("dx", _c_ptr), ("dweight", _c_ptr), ("dbias", _c_ptr),
+                ("tokens", _c_i64), ("n", _c_i64), ("ld_dy", _c_i64), ("ld_x", _c_i64),
+                ("ld_dx", _c_i64), ("dy_type", _c_i32), ("x_type", _c_i32),
+                ("param_type", _c_i32), ("dx_type", _c_i32), ("accumulate", _c_i32)]
+
+
+class intlora_embedding_job(ctypes.Structure):
+    _fields_ = [("table", _c_ptr), ("ids", _c_ptr), ("y", _c_ptr), ("invalid", _c_ptr),
+                ("vocab", _c_i64), ("n", _c_i64), ("tokens", _c_i64), ("ld_table", _c_i64),
+                ("ld_y", _c_i64), ("table_type", _c_i32), ("y_type", _c_i32),
+                ("id_bytes", _c_i32), ("scale", _c_f32)]
+
+
+class intlora_embedding_backward_job(ctypes.Structure):
+    _fields_ = [("dy", _c_ptr), ("ids", _c_ptr), ("dtable", _c_ptr), ("invalid", _c_ptr),
+                ("vocab", _c_i64), ("n", _c_i64), ("tokens", _c_i64), ("padding_id", _c_i64),
+                ("ld_dy", _c_i64), ("ld_dtable", _c_i64), ("dy_type", _c_i32),
+                ("dtable_type", _c_i32), ("id_bytes", _c_i32), ("accumulate", _c_i32),
+                ("scale", _c_f32)]
+
+
+class intlora_grad_job(ctypes.Structure):
+    _fields_ = [("g", _c_ptr), ("count", _c_i64), ("type", _c_i32)]
+
+
 _P = ctypes.POINTER
 _SIGNATURES = {
     "intlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -126,6 +162,23 @@ _SIGNATURES = {
                                         _c_ptr]),
     "intlora_int_gemm_batched": (ctypes.c_int, [_P(intlora_int_gemm_job), _c_i32, _c_i32,
                                                 _c_ptr]),
+    "intlora_layer_norm_batched": (ctypes.c_int, [_P(intlora_layer_norm_job), _c_i32, _c_ptr]),
+    "intlora_layer_norm_backward_workspace_size": (_c_size, [_P(intlora_layer_norm_backward_job),
+                                                             _c_i32]),
+    "intlora_layer_norm_backward_batched": (ctypes.c_int, [_P(intlora_layer_norm_backward_job),
+                                                           _c_i32, _c_ptr, _c_size, _c_ptr]),
+    "intlora_embedding_batched": (ctypes.c_int, [_P(intlora_embedding_job), _c_i32, _c_ptr]),
+    "intlora_embedding_backward_workspace_size": (_c_size, [_P(intlora_embedding_backward_job),
+                                                            _c_i32]),
+    "intlora_embedding_backward_batched": (ctypes.c_int, [_P(intlora_embedding_backward_job),
+                                                          _c_i32, _c_ptr, _c_size, _c_ptr]),
+    "intlora_grad_norm_workspace_size": (_c_size, [_P(intlora_grad_job), _c_i32]),
+    "intlora_grad_norm_batched": (ctypes.c_int, [_P(intlora_grad_job), _c_i32, _c_ptr, _c_ptr,
+                                                 _c_size, _c_ptr]),
+    "intlora_grad_clip_batched": (ctypes.c_int, [_P(intlora_grad_job), _c_i32, _c_f32, _c_ptr,
+                                                 _c_ptr]),
+    "intlora_clip_grad_norm_batched": (ctypes.c_int, [_P(intlora_grad_job), _c_i32, _c_f32, _c_ptr,
+                                                      _c_ptr, _c_size, _c_ptr]),
     "intlora_int_gemm": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64,
                                         _c_i32, _c_ptr, _c_ptr]),
 }
@@ -322,6 +375,195 @@ class TrainBackwardJob:
                                           _ptr(self.dA), _ptr(self.dB))
 
 
+# ---------------------------------------------------------------------------
+# descriptors of the operators around the linears. Element types, shapes and
+# strides travel to the library from the tensors, so they are checked here.
+# ---------------------------------------------------------------------------
+def _elem_type(name, t) -> int:
+    import torch
+    types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
+    return types[t.dtype]
+
+
+def _matrix(name, t, rows=None, cols=None) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or \
+            (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be 2-D, {rows if rows is not None else 'any'} x "
+                         f"{cols if cols is not None else 'any'}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(name, t, count, dtype=None) -> None:
+    if t is None:
+        return
+    if t.dim() != 1 or t.shape[0] != count or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {count}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _one_device(*tensors):
+    """The CUDA device that all tensors are on."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError("tensors must be on one CUDA device, got "
+                         f"{', '.join(sorted(str(d) for d in devices))}")
+    return next(iter(devices))
+
+
+def _counter(name, t) -> None:
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise TypeError(f"{name} must be an int32 tensor")
+
+
+def _ids(t) -> int:
+    import torch
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {t.dtype}")
+    return t.element_size()
+
+
+@dataclass
+class LayerNormJob:
+    x: object                       # fp32, bf16 or fp16 [tokens, n]
+    weight: object                  # [n] or None
+    bias: object                    # [n], the weight's type, or None
+    y: object                       # [tokens, n]
+    mean: object = None             # fp32 [tokens]
+    rstd: object = None             # fp32 [tokens]
+    eps: float = 1e-5
+
+    def to_c(self) -> intlora_layer_norm_job:
+        import torch
+        _one_device(self.x, self.weight, self.bias, self.y, self.mean, self.rstd)
+        ld_x = _matrix("x", self.x)
+        tokens, n = self.x.shape
+        ld_y = _matrix("y", self.y, tokens, n)
+        _vector("weight", self.weight, n)
+        _vector("bias", self.bias, n, None if self.weight is None else self.weight.dtype)
+        _vector("mean", self.mean, tokens, torch.float32)
+        _vector("rstd", self.rstd, tokens, torch.float32)
+        param = self.weight if self.weight is not None else self.bias
+        return intlora_layer_norm_job(_ptr(self.x), _ptr(self.weight), _ptr(self.bias),
+                                      _ptr(self.y), _ptr(self.mean), _ptr(self.rstd), tokens, n,
+                                      ld_x, ld_y, _elem_type("x", self.x),
+                                      TYPE_F32 if param is None else _elem_type("weight", param),
+                                      _elem_type("y", self.y), self.eps)
+
+    def device(self):
+        return self.x.device
+
+
+@dataclass
+class LayerNormBackwardJob:
+    dy: object                      # fp32, bf16 or fp16 [tokens, n]
+    x: object                       # [tokens, n], the forward's input
+    weight: object                  # [n] or None
+    mean: object                    # fp32 [tokens], from the forward
+    rstd: object                    # fp32 [tokens], from the forward
+    dx: object = None               # [tokens, n]
+    dweight: object = None          # fp32 [n]
+    dbias: object = None            # fp32 [n]
+    accumulate: bool = False        # add to dweight and dbias
+
+    def to_c(self) -> intlora_layer_norm_backward_job:
+        import torch
+        _one_device(self.dy, self.x, self.weight, self.mean, self.rstd, self.dx, self.dweight,
+                    self.dbias)
+        ld_x = _matrix("x", self.x)
+        tokens, n = self.x.shape
+        ld_dy = _matrix("dy", self.dy, tokens, n)
+        ld_dx = _matrix("dx", self.dx, tokens, n) if self.dx is not None else n
+        _vector("weight", self.weight, n)
+        _vector("mean", self.mean, tokens, torch.float32)
+        _vector("rstd", self.rstd, tokens, torch.float32)
+        _vector("dweight", self.dweight, n, torch.float32)
+        _vector("dbias", self.dbias, n, torch.float32)
+        return intlora_layer_norm_backward_job(
+            _ptr(self.dy), _ptr(self.x), _ptr(self.weight), _ptr(self.mean), _ptr(self.rstd),
+            _ptr(self.dx), _ptr(self.dweight), _ptr(self.dbias), tokens, n, ld_dy, ld_x, ld_dx,
+            _elem_type("dy", self.dy), _elem_type("x", self.x),
+            TYPE_F32 if self.weight is None else _elem_type("weight", self.weight),
+            TYPE_F32 if self.dx is None else _elem_type("dx", self.dx), int(self.accumulate))
+
+    def device(self):
+        return self.x.device
+
+
+@dataclass
+class EmbeddingJob:
+    table: object                   # fp32, bf16 or fp16 [vocab, n]
+    ids: object                     # int32 or int64 [tokens]
+    y: object                       # [tokens, n]
+    scale: float = 1.0
+    invalid: object = None          # int32 counter of ids outside the table
+
+    def to_c(self) -> intlora_embedding_job:
+        _one_device(self.table, self.ids, self.y, self.invalid)
+        ld_table = _matrix("table", self.table)
+        vocab, n = self.table.shape
+        id_bytes = _ids(self.ids)
+        _vector("ids", self.ids, self.ids.numel())
+        tokens = self.ids.numel()
+        ld_y = _matrix("y", self.y, tokens, n)
+        _counter("invalid", self.invalid)
+        return intlora_embedding_job(_ptr(self.table), _ptr(self.ids), _ptr(self.y),
+                                     _ptr(self.invalid), vocab, n, tokens, ld_table, ld_y,
+                                     _elem_type("table", self.table), _elem_type("y", self.y),
+                                     id_bytes, self.scale)
+
+    def device(self):
+        return self.table.device
+
+
+@dataclass
+class EmbeddingBackwardJob:
+    dy: object                      # fp32, bf16 or fp16 [tokens, n]
+    ids: object                     # int32 or int64 [tokens]
+    dtable: object                  # [vocab, n]
+    scale: float = 1.0
+    padding_id: int = -1            # its row gets no gradient (-1: none)
+    accumulate: bool = False        # add to the rows that have tokens; False: write all of dtable
+    invalid: object = None          # int32 counter of ids outside the table
+
+    def to_c(self) -> intlora_embedding_backward_job:
+        _one_device(self.dy, self.ids, self.dtable, self.invalid)
+        ld_dtable = _matrix("dtable", self.dtable)
+        vocab, n = self.dtable.shape
+        id_bytes = _ids(self.ids)
+        _vector("ids", self.ids, self.ids.numel())
+        tokens = self.ids.numel()
+        ld_dy = _matrix("dy", self.dy, tokens, n)
+        _counter("invalid", self.invalid)
+        return intlora_embedding_backward_job(
+            _ptr(self.dy), _ptr(self.ids), _ptr(self.dtable), _ptr(self.invalid), vocab, n, tokens,
+            self.padding_id, ld_dy, ld_dtable, _elem_type("dy", self.dy),
+            _elem_type("dtable", self.dtable), id_bytes, int(self.accumulate), self.scale)
+
+    def device(self):
+        return self.dtable.device
+
+
+@dataclass
+class GradJob:
+    g: object                       # fp32, bf16 or fp16, contiguous, any shape
+
+    def to_c(self) -> intlora_grad_job:
+        _one_device(self.g)
+        if not self.g.is_contiguous():
+            raise ValueError("g must be contiguous")
+        return intlora_grad_job(_ptr(self.g), self.g.numel(), _elem_type("g", self.g))
+
+    def device(self):
+        return self.g.device
+
+
 def _array(struct, items):
     if isinstance(items, Descriptors):
         if items.struct is not struct:
@@ -331,6 +573,32 @@ def _array(struct, items):
     for k, it in enumerate(items):
         arr[k] = it.to_c()
     return arr
+
+
+def _device_index(jobs) -> int:
+    indices = {j.device().index for j in jobs}
+    if len(indices) != 1:
+        raise ValueError(f"the jobs of a call must be on one device, got {sorted(indices)}")
+    return indices.pop()
+
+
+def _here(jobs) -> None:
+    """The library launches on the current device: the tensors must be there."""
+    import torch
+    if isinstance(jobs, Descriptors):
+        index = jobs.device_index
+    else:
+        index = _device_index(jobs) if len(jobs) else None
+    if index is not None and index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _norm_scalar(norm) -> int:
+    import torch
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device.type != "cuda":
+        raise TypeError("norm must be one fp32 element on a CUDA device")
+    return norm.data_ptr()
 
 
 class Descriptors:
@@ -351,6 +619,7 @@ class Descriptors:
                 raise TypeError("mixed descriptor types")
             self.arr[k] = it.to_c()
         self.count = len(items)
+        self.device_index = _device_index(items) if hasattr(items[0], "device") else None
 
     def __len__(self):
         return self.count
@@ -360,7 +629,12 @@ Descriptors._STRUCT = {AuxJob: intlora_aux_job, Layer: intlora_layer,
                        MergeOut: intlora_merge_out, SteJob: intlora_ste_job,
                        IntGemmJob: intlora_int_gemm_job, LinearJob: intlora_linear_job,
                        FakeQuantJob: intlora_fakequant_job,
-                       TrainBackwardJob: intlora_train_backward_job}
+                       TrainBackwardJob: intlora_train_backward_job,
+                       LayerNormJob: intlora_layer_norm_job,
+                       LayerNormBackwardJob: intlora_layer_norm_backward_job,
+                       EmbeddingJob: intlora_embedding_job,
+                       EmbeddingBackwardJob: intlora_embedding_backward_job,
+                       GradJob: intlora_grad_job}
 
 
 # ---------------------------------------------------------------------------
@@ -526,4 +800,73 @@ def intlora_train_backward_batched(jobs: Sequence[TrainBackwardJob], ws=None, st
 
 def intlora_fakequant_bf16_batched(jobs: Sequence[FakeQuantJob], stream=None) -> None:
     _check(lib().intlora_fakequant_bf16_batched(_array(intlora_fakequant_job, jobs), len(jobs),
+                                                _stream(stream)))
+
+
+def intlora_layer_norm_batched(jobs: Sequence[LayerNormJob], stream=None) -> None:
+    arr = _array(intlora_layer_norm_job, jobs)
+    _here(jobs)
+    _check(lib().intlora_layer_norm_batched(arr, len(jobs), _stream(stream)))
+
+
+def intlora_layer_norm_backward_workspace_size(jobs: Sequence[LayerNormBackwardJob]) -> int:
+    return lib().intlora_layer_norm_backward_workspace_size(
+        _array(intlora_layer_norm_backward_job, jobs), len(jobs))
+
+
+def intlora_layer_norm_backward_batched(jobs: Sequence[LayerNormBackwardJob], ws=None,
+                                        stream=None) -> None:
+    arr = _array(intlora_layer_norm_backward_job, jobs)
+    _here(jobs)
+    p, nb = _ws(ws)
+    _check(lib().intlora_layer_norm_backward_batched(arr, len(jobs), p, nb, _stream(stream)))
+
+
+def intlora_embedding_batched(jobs: Sequence[EmbeddingJob], stream=None) -> None:
+    arr = _array(intlora_embedding_job, jobs)
+    _here(jobs)
+    _check(lib().intlora_embedding_batched(arr, len(jobs), _stream(stream)))
+
+
+def intlora_embedding_backward_workspace_size(jobs: Sequence[EmbeddingBackwardJob]) -> int:
+    return lib().intlora_embedding_backward_workspace_size(
+        _array(intlora_embedding_backward_job, jobs), len(jobs))
+
+
+def intlora_embedding_backward_batched(jobs: Sequence[EmbeddingBackwardJob], ws=None,
+                                       stream=None) -> None:
+    arr = _array(intlora_embedding_backward_job, jobs)
+    _here(jobs)
+    p, nb = _ws(ws)
+    _check(lib().intlora_embedding_backward_batched(arr, len(jobs), p, nb, _stream(stream)))
+
+
+def intlora_grad_norm_workspace_size(jobs: Sequence[GradJob]) -> int:
+    return lib().intlora_grad_norm_workspace_size(_array(intlora_grad_job, jobs), len(jobs))
+
+
+def intlora_grad_norm_batched(jobs: Sequence[GradJob], norm, ws=None, stream=None) -> None:
+    """norm (fp32, one element) = sqrt(sum of g^2 over all jobs)."""
+    arr = _array(intlora_grad_job, jobs)
+    _here(jobs)
+    p, nb = _ws(ws)
+    _check(lib().intlora_grad_norm_batched(arr, len(jobs), _norm_scalar(norm), p, nb,
+                                           _stream(stream)))
+
+
+def intlora_grad_clip_batched(jobs: Sequence[GradJob], max_norm: float, norm, stream=None) -> None:
+    """g *= min(1, max_norm / (norm + 1e-6)) in place, norm as given."""
+    arr = _array(intlora_grad_job, jobs)
+    _here(jobs)
+    _check(lib().intlora_grad_clip_batched(arr, len(jobs), max_norm, _norm_scalar(norm),
+                                           _stream(stream)))
+
+
+def intlora_clip_grad_norm_batched(jobs: Sequence[GradJob], max_norm: float, norm, ws=None,
+                                   stream=None) -> None:
+    """Both: norm is written, and the gradients are clipped by it in place."""
+    arr = _array(intlora_grad_job, jobs)
+    _here(jobs)
+    p, nb = _ws(ws)
+    _check(lib().intlora_clip_grad_norm_batched(arr, len(jobs), max_norm, _norm_scalar(norm), p, nb,
                                                 _stream(stream)))
