@@ -1,16 +1,6 @@
-// Elements of fp32, bf16 and fp16 tensors whose type is known at run time.
-//
-// A thread's slice of a row is V chunks of 8 elements. It is fetched as raw
-// words first and converted afterwards, so that the loads of several tensors
-// are in flight together; the switch on the type is taken once per slice and
-// is uniform over the grid.
-//
-// Column of element e of chunk k for thread t of T that share a row:
-//   VEC:  (k T + t) 8 + e      16-byte loads and stores: rows start at a
-//                              16-byte boundary and hold a multiple of 8
-//                              elements
-//   else: (k 8 + e) T + t      one element per access, neighbouring threads
-//                              on neighbouring columns: any alignment, any n
+// Elements of fp32, bf16 and fp16 tensors: conversions, and accesses of one and
+// of eight elements. The type is a run-time value; where it is a constant the
+// compiler folds the choice.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -77,13 +67,28 @@ __device__ __forceinline__ uint4 pack8(const float* v, int type) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight consecutive elements from element i on (16-byte aligned).
+// 32 bytes from and to a 32-byte boundary in one access (two of 16 bytes would
+// touch every 32-byte sector twice).
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Eight consecutive elements from element i on, at a multiple of 8 elements
+// (32 bytes of fp32, 16 of a 16-bit type).
 __device__ __forceinline__ void load8(const void* p, int64_t i, int type, float* v) {
   if (type == kF32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    uint32_t w[8];
+    load32(static_cast<const float*>(p) + i, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
   } else {
     const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -92,94 +97,18 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int type, float*
 }
 __device__ __forceinline__ void store8(void* p, int64_t i, int type, const float* v) {
   if (type == kF32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[e]);
+    store32(static_cast<float*>(p) + i, w);
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8(v, type);
   }
 }
 
-template <bool VEC>
-__device__ __forceinline__ int slice_col(int k, int e, int t, int T) {
-  return VEC ? (k * T + t) * 8 + e : (k * 8 + e) * T + t;
-}
-
-// Raw words of one thread's slice of a row. VEC: a chunk of fp32 takes 8
-// words, of a 16-bit type 4; else: one word per element.
-template <int V>
-struct RawSlice {
-  uint32_t w[8 * V];
-};
-
-// Columns at or past n read as zero.
-template <int V, bool VEC>
-__device__ __forceinline__ void load_slice(RawSlice<V>& r, const void* row, int type, int n, int t, int T) {
-  if (type == kF32) {
-    const float* p = static_cast<const float*>(row);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (VEC) {
-        const int c = slice_col<VEC>(k, 0, t, T);
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (c < n) {
-          a = *reinterpret_cast<const uint4*>(p + c);
-          b = *reinterpret_cast<const uint4*>(p + c + 4);
-        }
-        r.w[8 * k] = a.x; r.w[8 * k + 1] = a.y; r.w[8 * k + 2] = a.z; r.w[8 * k + 3] = a.w;
-        r.w[8 * k + 4] = b.x; r.w[8 * k + 5] = b.y; r.w[8 * k + 6] = b.z; r.w[8 * k + 7] = b.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = slice_col<VEC>(k, e, t, T);
-          r.w[8 * k + e] = c < n ? __float_as_uint(p[c]) : 0u;
-        }
-      }
-    }
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(row);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (VEC) {
-        const int c = slice_col<VEC>(k, 0, t, T);
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (c < n) a = *reinterpret_cast<const uint4*>(p + c);
-        r.w[8 * k] = a.x; r.w[8 * k + 1] = a.y; r.w[8 * k + 2] = a.z; r.w[8 * k + 3] = a.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = slice_col<VEC>(k, e, t, T);
-          r.w[8 * k + e] = c < n ? p[c] : 0u;
-        }
-      }
-    }
-  }
-}
-
-// Chunk k of a raw slice as floats.
-template <int V, bool VEC>
-__device__ __forceinline__ void slice_chunk(const RawSlice<V>& r, int type, int k, float* v) {
-  if (VEC && type != kF32) {
-    unpack8(&r.w[8 * k], type, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = elem_from_bits(r.w[8 * k + e], type);
-  }
-}
-
-// Writes chunk k of a thread's slice (columns at or past n are skipped).
-template <bool VEC>
-__device__ __forceinline__ void store_chunk(void* row, int type, int n, int t, int T, int k, const float* v) {
-  if (VEC) {
-    const int c = slice_col<VEC>(k, 0, t, T);
-    if (c < n) store8(row, c, type, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = slice_col<VEC>(k, e, t, T);
-      if (c < n) store_elem(row, c, type, v[e]);
-    }
-  }
+// Rows that start at multiples of 8 elements.
+inline bool rows_by_8(const void* p, int64_t ld, int type) {
+  return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(8 * elem_bytes(type)) == 0 && ld % 8 == 0;
 }
 
 __device__ __forceinline__ const void* row_ptr(const void* p, int64_t row, int64_t ld, int type) {

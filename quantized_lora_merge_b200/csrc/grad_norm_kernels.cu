@@ -28,19 +28,20 @@ constexpr int kThreads = 256;
 constexpr int kPerThread = 32;                 // elements of a chunk a thread holds
 constexpr int64_t kChunk = kThreads * kPerThread;
 constexpr int kMaxBlocks = kSms * 4;
-constexpr int kMaxSpans = 512;                 // tensors per launch
+constexpr int kMaxSpans = 512, kFewSpans = 64; // tensors per launch
 
-// Tensors of one launch, by value: no table in device memory.
+// Tensors of one launch, by value: no table in device memory. 14 bytes each, since
+// a launch copies them: what a chunk needs beside its tensor's first element is
+// the length of the last chunk and the type.
 template <int N>
 struct Spans {
   void* g[N];
-  int64_t count[N];
   uint32_t begin[N + 1];                       // first chunk of each tensor
-  uint8_t type[N];
+  uint16_t last[N];                            // (elements of the last chunk - 1) | type << 14
   int32_t spans;
   uint32_t chunks;
-  double* partial;                             // of this launch's first block
 };
+static_assert(kChunk <= (1 << 14), "a chunk's length fits beside the type");
 
 // Sum of squares of a thread's values. Squares of fp32 and bf16 values above
 // 2^64 or below 2^-63 leave the range of fp32, so a sum that is not well inside
@@ -59,7 +60,7 @@ __device__ __forceinline__ double square_sum(const float (&v)[kPerThread]) {
 }
 
 // A thread's part of a chunk of a tensor: 4 groups of 8 elements where the
-// tensor starts at a 16-byte boundary, else single elements.
+// tensor starts at a multiple of 8 elements, else single elements.
 struct Piece {
   void* g;
   int64_t first;                               // element of the chunk's begin
@@ -72,9 +73,9 @@ __device__ __forceinline__ Piece piece_of(const Spans<N>& b, int span, uint32_t 
   Piece p;
   p.g = b.g[span];
   p.first = static_cast<int64_t>(chunk - b.begin[span]) * kChunk;
-  p.len = static_cast<int>(min(kChunk, b.count[span] - p.first));
-  p.type = b.type[span];
-  p.vec = (reinterpret_cast<uintptr_t>(p.g) & 15u) == 0;
+  p.len = chunk + 1 < b.begin[span + 1] ? static_cast<int>(kChunk) : (b.last[span] & 0x3fff) + 1;
+  p.type = b.last[span] >> 14;
+  p.vec = reinterpret_cast<uintptr_t>(p.g) % (8 * elem_bytes(p.type)) == 0;
   return p;
 }
 __device__ __forceinline__ void load_piece(const Piece& p, float (&v)[kPerThread]) {
@@ -131,7 +132,7 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ Spans<N> b) {
+__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ Spans<N> b, double* partial) {
   const uint32_t end = stretch(b.chunks, blockIdx.x + 1);
   uint32_t chunk = stretch(b.chunks, blockIdx.x);
   int span = chunk < end ? span_of(b, chunk) : 0;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
     sum += square_sum(v);
   }
   sum = block_sum(sum);
-  if (threadIdx.x == 0) b.partial[blockIdx.x] = sum;
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
 // The norm from all partial sums, the same in every block.
@@ -196,12 +197,12 @@ int32_t fill(const intlora_grad_job* jobs, int32_t k0, int32_t count, Spans<N>* 
   int32_t n = 0, k = k0;
   uint32_t chunks = 0;
   for (; k < count && n < N; ++k) {
-    if (jobs[k].count == 0) continue;
+    const uint64_t c = static_cast<uint64_t>(jobs[k].count);
+    if (c == 0) continue;
     b->g[n] = jobs[k].g;
-    b->count[n] = jobs[k].count;
-    b->type[n] = static_cast<uint8_t>(jobs[k].type);
     b->begin[n] = chunks;
-    chunks += static_cast<uint32_t>((jobs[k].count + kChunk - 1) / kChunk);
+    b->last[n] = static_cast<uint16_t>(((c - 1) % kChunk) | (static_cast<uint64_t>(jobs[k].type) << 14));
+    chunks += static_cast<uint32_t>((c + kChunk - 1) / kChunk);
     ++n;
   }
   b->begin[n] = chunks;
@@ -210,64 +211,79 @@ int32_t fill(const intlora_grad_job* jobs, int32_t k0, int32_t count, Spans<N>* 
   return k;
 }
 
-// Blocks of the launch that takes jobs[*k ..), which moves on behind it.
-int64_t launch_blocks(const intlora_grad_job* jobs, int32_t* k, int32_t count) {
-  int64_t chunks = 0;
-  for (int32_t n = 0; *k < count && n < kMaxSpans; ++*k) {
-    if (jobs[*k].count == 0) continue;
-    chunks += (jobs[*k].count + kChunk - 1) / kChunk;
-    ++n;
+// Calls f(table, blocks) for launch after launch over the jobs. Few tensors get
+// a smaller table: it is part of the launch.
+template <int N, typename F>
+cudaError_t each_launch(const intlora_grad_job* jobs, int32_t count, F f) {
+  static thread_local Spans<N> b;
+  for (int32_t k = 0; k < count;) {
+    k = fill(jobs, k, count, &b);
+    const cudaError_t e = f(b, blocks_of(b.chunks));
+    if (e != cudaSuccess) return e;
   }
-  return blocks_of(chunks);
+  return cudaSuccess;
 }
-
-int64_t partials_of(const intlora_grad_job* jobs, int32_t count) {
-  int64_t total = 0;
-  for (int32_t k = 0; k < count;) total += launch_blocks(jobs, &k, count);
-  return total;
+template <typename F>
+cudaError_t each_launch(const intlora_grad_job* jobs, int32_t count, F f) {
+  return count <= kFewSpans ? each_launch<kFewSpans>(jobs, count, f) : each_launch<kMaxSpans>(jobs, count, f);
 }
 
 }  // namespace
 
-size_t grad_norm_ws(const intlora_grad_job* jobs, int32_t count) {
-  return (static_cast<size_t>(partials_of(jobs, count)) * sizeof(double) + 255) / 256 * 256;
+// One fp64 partial sum per block of every launch, in launch order.
+int64_t grad_norm_partials(const intlora_grad_job* jobs, int32_t count) {
+  int64_t total = 0;
+  for (int32_t k = 0; k < count;) {
+    int64_t chunks = 0;
+    for (int32_t n = 0; k < count && n < kMaxSpans; ++k) {
+      if (jobs[k].count == 0) continue;
+      chunks += (jobs[k].count + kChunk - 1) / kChunk;
+      ++n;
+    }
+    total += blocks_of(chunks);
+  }
+  return total;
 }
 
 cudaError_t launch_grad_squares(const intlora_grad_job* jobs, int32_t count, void* ws, cudaStream_t s) {
   double* partial = static_cast<double*>(ws);
-  static thread_local Spans<kMaxSpans> b;
-  for (int32_t k = 0; k < count;) {
-    k = fill(jobs, k, count, &b);
-    b.partial = partial;
-    const int64_t blocks = blocks_of(b.chunks);
-    grad_squares_kernel<kMaxSpans><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b);
-    const cudaError_t e = counted(cudaGetLastError());
-    if (e != cudaSuccess) return e;
+  return each_launch(jobs, count, [&](const auto& b, int64_t blocks) {
+    grad_squares_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, partial);
     partial += blocks;
-  }
-  return cudaSuccess;
+    return counted(cudaGetLastError());
+  });
 }
 
-cudaError_t launch_grad_norm_finish(const intlora_grad_job* jobs, int32_t count, const void* ws, float* norm,
-                                    cudaStream_t s) {
-  grad_norm_finish_kernel<<<1, kThreads, 0, s>>>(static_cast<const double*>(ws), partials_of(jobs, count), norm);
+cudaError_t launch_grad_norm_finish(int64_t partials, const void* ws, float* norm, cudaStream_t s) {
+  grad_norm_finish_kernel<<<1, kThreads, 0, s>>>(static_cast<const double*>(ws), partials, norm);
   return counted(cudaGetLastError());
 }
 
-cudaError_t launch_grad_clip(const intlora_grad_job* jobs, int32_t count, float max_norm, const void* ws, float* norm,
-                             cudaStream_t s) {
-  const int64_t partials = ws != nullptr ? partials_of(jobs, count) : 0;
-  static thread_local Spans<kMaxSpans> b;
-  for (int32_t k = 0; k < count;) {
-    const int write = k == 0;
-    k = fill(jobs, k, count, &b);
-    b.partial = nullptr;
-    grad_clip_kernel<kMaxSpans><<<static_cast<unsigned>(blocks_of(b.chunks)), kThreads, 0, s>>>(
-        b, static_cast<const double*>(ws), partials, max_norm, norm, write);
+cudaError_t launch_grad_clip(const intlora_grad_job* jobs, int32_t count, float max_norm, const void* ws,
+                             int64_t partials, float* norm, cudaStream_t s) {
+  int write = 1;                               // the first launch writes the norm
+  return each_launch(jobs, count, [&](const auto& b, int64_t blocks) {
+    grad_clip_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, static_cast<const double*>(ws), partials,
+                                                                       max_norm, norm, write);
+    write = 0;
+    return counted(cudaGetLastError());
+  });
+}
+
+cudaError_t launch_clip_grad_norm(const intlora_grad_job* jobs, int32_t count, float max_norm, void* ws,
+                                  int64_t partials, float* norm, cudaStream_t s) {
+  if (count > kMaxSpans) {                     // the whole norm comes before the first clipping
+    const cudaError_t e = launch_grad_squares(jobs, count, ws, s);
+    return e != cudaSuccess ? e : launch_grad_clip(jobs, count, max_norm, ws, partials, norm, s);
+  }
+  return each_launch(jobs, count, [&](const auto& b, int64_t blocks) {   // one table for both
+    grad_squares_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, static_cast<double*>(ws));
     const cudaError_t e = counted(cudaGetLastError());
     if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+    grad_clip_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, static_cast<const double*>(ws), partials,
+                                                                       max_norm, norm, 1);
+    return counted(cudaGetLastError());
+  });
 }
 
 }  // namespace intlora

@@ -68,15 +68,18 @@ size_t embedding_backward_ws(int64_t tokens, int64_t n);
 cudaError_t launch_embedding_backward(const EmbeddingBackwardJob& j, void* ws, cudaStream_t s);
 
 // Gradient norm and clipping (grad_norm_kernels.cu).
-size_t grad_norm_ws(const intlora_grad_job* jobs, int32_t count);
+// Partial sums, of 8 bytes each in ws.
+int64_t grad_norm_partials(const intlora_grad_job* jobs, int32_t count);
 // Sum of squares over all tensors, as partial sums in ws.
 cudaError_t launch_grad_squares(const intlora_grad_job* jobs, int32_t count, void* ws, cudaStream_t s);
 // *norm = root of the partial sums' total.
-cudaError_t launch_grad_norm_finish(const intlora_grad_job* jobs, int32_t count, const void* ws, float* norm,
-                                    cudaStream_t s);
+cudaError_t launch_grad_norm_finish(int64_t partials, const void* ws, float* norm, cudaStream_t s);
 // g *= min(1, max_norm / (norm + 1e-6)). ws not nullptr: the norm comes from
 // the partial sums and is written to *norm; else it is read from *norm.
-cudaError_t launch_grad_clip(const intlora_grad_job* jobs, int32_t count, float max_norm, const void* ws, float* norm,
-                             cudaStream_t s);
+cudaError_t launch_grad_clip(const intlora_grad_job* jobs, int32_t count, float max_norm, const void* ws,
+                             int64_t partials, float* norm, cudaStream_t s);
+// launch_grad_squares and launch_grad_clip; count >= 1.
+cudaError_t launch_clip_grad_norm(const intlora_grad_job* jobs, int32_t count, float max_norm, void* ws,
+                                  int64_t partials, float* norm, cudaStream_t s);
 
 }  // namespace intlora

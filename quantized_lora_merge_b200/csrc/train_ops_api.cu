@@ -188,17 +188,17 @@ struct Extent {
   uintptr_t begin, end;
   int32_t job;
 };
+Extent extent_of(const intlora_grad_job* jobs, int32_t k) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(jobs[k].g);
+  return Extent{b, b + static_cast<uintptr_t>(jobs[k].count) * static_cast<uintptr_t>(elem_bytes(jobs[k].type)), k};
+}
 intlora_status check_disjoint(const intlora_grad_job* jobs, int32_t count) {
-  const auto extent = [&](int32_t k) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(jobs[k].g);
-    return Extent{b, b + static_cast<uintptr_t>(jobs[k].count) * static_cast<uintptr_t>(elem_bytes(jobs[k].type)), k};
-  };
   // tensors in the order of their addresses, as an arena has them, need no sort
   bool ascending = true;
   uintptr_t end = 0;
   for (int32_t k = 0; k < count && ascending; ++k) {
     if (jobs[k].count == 0) continue;
-    const Extent e = extent(k);
+    const Extent e = extent_of(jobs, k);
     ascending = e.begin >= end;
     end = e.end;
   }
@@ -207,7 +207,7 @@ intlora_status check_disjoint(const intlora_grad_job* jobs, int32_t count) {
   if (!all) return fail(INTLORA_ERR_UNSUPPORTED, "out of host memory for %d gradient jobs", count);
   int32_t n = 0;
   for (int32_t k = 0; k < count; ++k)
-    if (jobs[k].count > 0) all[n++] = extent(k);
+    if (jobs[k].count > 0) all[n++] = extent_of(jobs, k);
   std::sort(all.get(), all.get() + n, [](const Extent& a, const Extent& b) { return a.begin < b.begin; });
   for (int32_t k = 1; k < n; ++k)
     if (all[k].begin < all[k - 1].end)
@@ -215,6 +215,8 @@ intlora_status check_disjoint(const intlora_grad_job* jobs, int32_t count) {
                   std::max(all[k - 1].job, all[k].job));
   return INTLORA_OK;
 }
+
+size_t partial_bytes(int64_t partials) { return (static_cast<size_t>(partials) * sizeof(double) + 255) / 256 * 256; }
 
 intlora_status check_max_norm(float max_norm) {
   if (!(max_norm >= 0.0f) || !std::isfinite(max_norm))
@@ -319,17 +321,18 @@ intlora_status intlora_embedding_backward_batched(const intlora_embedding_backwa
 
 size_t intlora_grad_norm_workspace_size(const intlora_grad_job* jobs, int32_t count) {
   if (jobs == nullptr || count <= 0 || check_grads(jobs, count) != INTLORA_OK) return 0;
-  return grad_norm_ws(jobs, count);
+  return partial_bytes(grad_norm_partials(jobs, count));
 }
 
 intlora_status intlora_grad_norm_batched(const intlora_grad_job* jobs, int32_t count, float* norm, void* ws,
                                          size_t ws_bytes, void* stream) {
   intlora_status s = check_grads(jobs, count);
   if (s != INTLORA_OK || (s = check_norm(norm)) != INTLORA_OK) return s;
-  if ((s = check_ws(ws, ws_bytes, intlora_grad_norm_workspace_size(jobs, count))) != INTLORA_OK) return s;
+  const int64_t partials = grad_norm_partials(jobs, count);
+  if ((s = check_ws(ws, ws_bytes, partial_bytes(partials))) != INTLORA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_grad_squares(jobs, count, ws, st);
-  if (e == cudaSuccess) e = launch_grad_norm_finish(jobs, count, ws, norm, st);
+  if (e == cudaSuccess) e = launch_grad_norm_finish(partials, ws, norm, st);
   return e == cudaSuccess ? INTLORA_OK : cuda_fail(e, "gradient norm launch");
 }
 
@@ -339,7 +342,7 @@ intlora_status intlora_grad_clip_batched(const intlora_grad_job* jobs, int32_t c
   if (s != INTLORA_OK || (s = check_max_norm(max_norm)) != INTLORA_OK || (s = check_norm(norm)) != INTLORA_OK ||
       (s = check_disjoint(jobs, count)) != INTLORA_OK)
     return s;
-  const cudaError_t e = launch_grad_clip(jobs, count, max_norm, nullptr, const_cast<float*>(norm),
+  const cudaError_t e = launch_grad_clip(jobs, count, max_norm, nullptr, 0, const_cast<float*>(norm),
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? INTLORA_OK : cuda_fail(e, "gradient clipping launch");
 }
@@ -350,14 +353,11 @@ intlora_status intlora_clip_grad_norm_batched(const intlora_grad_job* jobs, int3
   if (s != INTLORA_OK || (s = check_max_norm(max_norm)) != INTLORA_OK || (s = check_norm(norm)) != INTLORA_OK ||
       (s = check_disjoint(jobs, count)) != INTLORA_OK)
     return s;
-  if ((s = check_ws(ws, ws_bytes, intlora_grad_norm_workspace_size(jobs, count))) != INTLORA_OK) return s;
+  const int64_t partials = grad_norm_partials(jobs, count);
+  if ((s = check_ws(ws, ws_bytes, partial_bytes(partials))) != INTLORA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (count == 0) {
-    const cudaError_t e = launch_grad_norm_finish(jobs, count, ws, norm, st);
-    return e == cudaSuccess ? INTLORA_OK : cuda_fail(e, "gradient norm launch");
-  }
-  cudaError_t e = launch_grad_squares(jobs, count, ws, st);
-  if (e == cudaSuccess) e = launch_grad_clip(jobs, count, max_norm, ws, norm, st);
+  const cudaError_t e = count == 0 ? launch_grad_norm_finish(0, ws, norm, st)
+                                   : launch_clip_grad_norm(jobs, count, max_norm, ws, partials, norm, st);
   return e == cudaSuccess ? INTLORA_OK : cuda_fail(e, "gradient clipping launch");
 }
 
