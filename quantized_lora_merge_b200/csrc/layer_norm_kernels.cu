@@ -391,20 +391,25 @@ __device__ __forceinline__ void fetch_row(uint32_t stage, const char* src, bool 
   } else {
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15u);
     const int end = shift + n * es;            // of the row, from its first granule on
-    // one granule more: zeros, over what a row that started later left there
-    for (int g = t * 16; g < end + 16; g += T * 16) {
-      if (g == 0 && shift != 0 && first_row) {
-        const int last = min(end, 16);
-        for (int b = shift; b < last; b += es) {
-          if (es == 4)
-            *reinterpret_cast<uint32_t*>(smem() + stage + b) = *reinterpret_cast<const uint32_t*>(src + (b - shift));
-          else
-            *reinterpret_cast<uint16_t*>(smem() + stage + b) = *reinterpret_cast<const uint16_t*>(src + (b - shift));
-        }
-      } else {
-        const int bytes = max(0, min(16, end - g));
-        copy16_cut(stage + g, bytes > 0 ? src - shift + g : src - shift + end / 32 * 16, bytes);
+    const char* from = src - shift;
+    const bool cut = first_row && shift != 0;  // the first granule begins before the tensor
+    const int whole = end / 16 * 16;
+#pragma unroll 1
+    for (int g = (t == 0 && cut ? T : t) * 16; g < whole; g += T * 16) copy16(stage + g, from + g);
+    if (t == 0 && cut) {
+      for (int b = shift; b < min(end, 16); b += es) {
+        if (es == 4)
+          *reinterpret_cast<uint32_t*>(smem() + stage + b) = *reinterpret_cast<const uint32_t*>(from + b);
+        else
+          *reinterpret_cast<uint16_t*>(smem() + stage + b) = *reinterpret_cast<const uint16_t*>(from + b);
       }
+    }
+    // the granule in which the row ends, filled up with zeros, and one of zeros
+    // over what a row that started later in its first granule left there
+    if (t == T - 1) {
+      const bool open = end > whole && !(cut && whole == 0);
+      if (open) copy16_cut(stage + whole, from + whole, end - whole);
+      copy16_cut(stage + (end + 15) / 16 * 16, from, 0);
     }
   }
 }
@@ -928,7 +933,7 @@ bool row_shape(const RowWant& q, RowShape* best) {
   double least = -1.0;
   for (int v : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
     if (v > q.max_v) break;
-    if (!q.vec && v != 1 && v != 2 && v != 4 && v != 8) continue;
+    if (!q.vec && v != 1 && v != 2 && v != 4 && v != 8 && !(v == 6 && q.second_type >= 0)) continue;
     RowShape r;
     const int64_t t = (chunks + 32 * v - 1) / (32 * v) * 32;
     if (t > kBlock) continue;
@@ -1027,6 +1032,7 @@ cudaError_t bwd_by_v(const LayerNormBackwardJob& j, const RowShape& r, bool vec,
     case -1: return launch_bwd<TX, TY, 1, false>(j, r, grid, smem, partial, s);
     case -2: return launch_bwd<TX, TY, 2, false>(j, r, grid, smem, partial, s);
     case -4: return launch_bwd<TX, TY, 4, false>(j, r, grid, smem, partial, s);
+    case -6: return launch_bwd<TX, TY, 6, false>(j, r, grid, smem, partial, s);
     case -8: return launch_bwd<TX, TY, 8, false>(j, r, grid, smem, partial, s);
   }
   return cudaErrorInvalidConfiguration;
@@ -1052,8 +1058,9 @@ cudaError_t launch_layer_norm(const LayerNormJob& j, cudaStream_t s) {
   const bool vec = rows_aligned(j.x, j.ld_x, j.n, j.x_type) && rows_aligned(j.y, j.ld_y, j.n, j.y_type) &&
                    reinterpret_cast<uintptr_t>(j.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(j.bias) % 16 == 0;
   RowShape r;
-  // Few rows: no ring.
-  if (j.tokens <= kSms && single_row_shape(j.n, &r)) {
+  // Few rows: no ring. Single elements leave the ring a smaller lead: 1031 x 5003
+  // takes 12.4 us this way and 18.7 with it.
+  if (j.tokens <= (vec ? 1 : 8) * kSms && single_row_shape(j.n, &r)) {
     const unsigned grid = static_cast<unsigned>((j.tokens + r.teams - 1) / r.teams);
     const int threads = r.threads();
     switch (r.V) {
@@ -1129,7 +1136,10 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardJob& j, void* ws, 
                      (j.dx == nullptr || rows_aligned(j.dx, j.ld_dx, j.n, j.dx_type)) &&
                      reinterpret_cast<uintptr_t>(j.weight) % 16 == 0;
     RowShape r;
-    if (!row_shape(RowWant{j.tokens, j.n, vec, kBwdMaxV, j.x_type, j.dy_type, 1}, &r)) return cudaErrorInvalidConfiguration;
+    // single elements take more registers: V = 8 spills (3000 x 5003: 65 us, V = 6 58)
+    if (!row_shape(RowWant{j.tokens, j.n, vec, vec ? kBwdMaxV : 6, j.x_type, j.dy_type, 1}, &r) &&
+        !row_shape(RowWant{j.tokens, j.n, vec, kBwdMaxV, j.x_type, j.dy_type, 1}, &r))
+      return cudaErrorInvalidConfiguration;
     // the joined sums take the place of ring and parameters
     const size_t join = static_cast<size_t>(r.T >= 32 ? r.teams : r.threads() / 32) * 2 * slot_columns(r) * sizeof(float);
     const size_t smem = std::max(static_cast<size_t>(r.params) + static_cast<size_t>(slot_columns(r)) * sizeof(float), join);
