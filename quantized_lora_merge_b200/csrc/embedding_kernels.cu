@@ -612,14 +612,14 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Words of up to kFewTokens tokens, the most of a text: no chunk, positions in
-// shared memory, 32-bit arithmetic, two strips at once; every token row of the
-// word is in flight together. (By the general way below, 50 instructions an
+// shared memory, 32-bit arithmetic, two strips at once, up to four token rows in
+// flight. (By the general way below, 50 instructions an
 // element, the touched rows of 16384 tokens of different words took 133 us.)
-constexpr int kFewTokens = 4;
+constexpr int kFewTokens = 16;
 template <int TYPE, bool VEC, bool ACC, bool OUT32>
 __device__ __forceinline__ void few_tokens(const EmbeddingBackwardJob& j, const uint32_t* pos, int count, uint32_t v,
                                            int64_t c0) {
-  constexpr int W = VEC ? 8 : 1, C = VEC ? 2 : 4, U = TYPE == kF32 && VEC ? 2 : kFewTokens;
+  constexpr int W = VEC ? 8 : 1, C = VEC ? 2 : 4, U = TYPE == kF32 && VEC ? 2 : 4;
   constexpr int kWords = VEC ? (TYPE == kF32 ? 8 : 4) : 1;
   const int to = OUT32 ? kF32 : j.dtable_type;
   const int lane = threadIdx.x & 31;
@@ -635,9 +635,8 @@ __device__ __forceinline__ void few_tokens(const EmbeddingBackwardJob& j, const 
     if constexpr (VEC) load8(dst, c + 32 * W * k, to, old[k]);
     else old[k][0] = load_elem(dst, c + 32 * W * k, to);
   }
-#pragma unroll
-  for (int i = 0; i < kFewTokens; i += U) {
-    if (i >= count) break;
+#pragma unroll 1
+  for (int i = 0; i < count; i += U) {
     uint32_t w[U][C][kWords];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
