@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kThreads)
 // shared memory, 32-bit arithmetic, two strips at once, up to four token rows in
 // flight. (By the general way below, 50 instructions an
 // element, the touched rows of 16384 tokens of different words took 133 us.)
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 8;
 template <int TYPE, bool VEC, bool ACC, bool OUT32>
 __device__ __forceinline__ void few_tokens(const EmbeddingBackwardJob& j, const uint32_t* pos, int count, uint32_t v,
                                            int64_t c0) {
@@ -635,8 +635,9 @@ __device__ __forceinline__ void few_tokens(const EmbeddingBackwardJob& j, const 
     if constexpr (VEC) load8(dst, c + 32 * W * k, to, old[k]);
     else old[k][0] = load_elem(dst, c + 32 * W * k, to);
   }
-#pragma unroll 1
-  for (int i = 0; i < count; i += U) {
+#pragma unroll
+  for (int i = 0; i < kFewTokens; i += U) {
+    if (i >= count) break;
     uint32_t w[U][C][kWords];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -682,113 +683,135 @@ __device__ __forceinline__ void few_tokens(const EmbeddingBackwardJob& j, const 
   }
 }
 
-// The touched rows. A block looks at `span` (up to kMaxRows) sorted positions and
-// owns the words that begin there, at kBlockStrips strips of their columns. Words with
-// more than kFewTokens tokens: a warp takes one strip of one word, the tokens
-// before and behind whole chunks, then the whole chunks' sums. Words with more than kManyRows of these are shared by the
-// block's warps, contiguous parts each (one warp alone took 80 us for a word with
-// 1500 of 16384 tokens, while all others waited).
-constexpr int kPositions = 128;                // kept in shared memory, from the block's first on
-constexpr int kBlockStrips = 4, kManyRows = 16;
+// Sorted positions that a block of the touched pass keeps in shared memory, and
+// the words that begin among the first `span` of them.
+constexpr int kPositions = 128;
+struct Words {
+  int64_t first[kPositions], last[kPositions]; // sorted positions of a word
+  uint32_t word[kPositions];
+  uint32_t pos[kPositions], key[kPositions + 1];   // key[i + 1]: position p0 + i
+  int count;
+};
+// Words with at least `least` tokens, in no particular order.
+__device__ __forceinline__ void find_words(Words& w, const EmbeddingBackwardJob& j, const uint32_t* key,
+                                           const uint32_t* pos, int64_t p0, int span, int least) {
+  static_assert(kThreads == 2 * kPositions, "a thread an entry");
+  const int t = threadIdx.x;
+  const int near = static_cast<int>(min(static_cast<int64_t>(kPositions), j.tokens - p0));
+  if (t < kPositions) {
+    if (t < near) w.key[t + 1] = key[p0 + t];
+    if (t == 0) {
+      w.key[0] = p0 > 0 ? key[p0 - 1] : kNoRow;
+      w.count = 0;
+    }
+  } else if (t - kPositions < near) {
+    w.pos[t - kPositions] = pos[p0 + t - kPositions];
+  }
+  __syncthreads();
+  if (t < span && t < near) {
+    const uint32_t x = w.key[t + 1];
+    if (x < j.vocab && w.key[t] != x) {
+      int end = t + 1;
+      while (end < near && w.key[end + 1] == x) ++end;
+      int64_t e = p0 + end;
+      if (end == near && e < j.tokens)         // it goes on behind what is here
+        e += run_rank<int64_t>(key + e, j.tokens - e, x, true);
+      if (e - (p0 + t) >= least) {
+        const int at = atomicAdd(&w.count, 1);
+        w.first[at] = p0 + t;
+        w.last[at] = e;
+        w.word[at] = x;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The rows that make up a word's sum: the tokens before and behind whole chunks,
+// then the whole chunks' sums.
+struct WordRows {
+  int64_t a, head, loose, skip, lo, count;
+  __device__ __forceinline__ WordRows(int64_t first, int64_t last) {
+    const int64_t hi = last / kChunk;
+    a = first;
+    lo = (first + kChunk - 1) / kChunk;
+    const bool whole = lo < hi;
+    head = whole ? lo * kChunk - first : last - first;
+    loose = whole ? head + last - hi * kChunk : head;
+    skip = whole ? hi * kChunk - head : first;             // from there on the positions behind the chunks
+    count = loose + (whole ? hi - lo : 0);
+  }
+};
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void add_word(Strip<VEC>& s, const EmbeddingBackwardJob& j, const Words& words,
+                                         const uint32_t* pos, int64_t p0, const float* partial, const WordRows& w,
+                                         int64_t from, int64_t to, int64_t c0) {
+  add_rows<TYPE, VEC, kRowsAhead<TYPE>>(s, j.dy, j.ld_dy, min(to, w.loose) - from, c0, j.n, [&](int64_t i) {
+    const int64_t p = (from + i < w.head ? w.a : w.skip) + from + i;
+    return p - p0 < kPositions ? words.pos[p - p0] : __ldg(pos + p);
+  });
+  const int64_t begin = max(from, w.loose);
+  add_rows<kF32, VEC, kRowsAhead<kF32>>(s, partial, j.n, to - begin, c0, j.n,
+                                        [&](int64_t i) { return static_cast<uint32_t>(w.lo + (begin - w.loose) + i); });
+}
+
+// The touched rows. The first heavy_blocks blocks each look at kPositions sorted
+// positions and one strip of columns, for words of more than kManyRows rows that
+// begin there: the block's warps add contiguous parts. (One warp alone took 80 us
+// for a word with 1500 of 16384 tokens, while all others waited; a block for 8
+// strips of it 40 us.) The others look at `span` (up to kMaxRows) positions and
+// kBlockStrips strips: words of up to kFewTokens tokens, a warp two strips at
+// once, and those between, a warp a strip.
+constexpr int kBlockStrips = 8, kManyRows = 16;
 template <int TYPE, bool VEC, bool ACC, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 4)
     embedding_touched_kernel(const __grid_constant__ EmbeddingBackwardJob j, const uint32_t* key, const uint32_t* pos,
-                             const float* partial, int span, int strips, unsigned groups) {
-  __shared__ int64_t first[kMaxRows], last[kMaxRows];
-  __shared__ uint32_t word[kMaxRows], near_pos[kPositions];
+                             const float* partial, int span, int strips, unsigned groups, unsigned heavy_blocks) {
+  __shared__ Words words;
   __shared__ float part[kWarps][strip_columns(VEC)];
-  __shared__ int words;
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x / groups) * span;
-  if (threadIdx.x >= kThreads - kPositions) {
-    const int i = threadIdx.x - (kThreads - kPositions);
-    if (p0 + i < j.tokens) near_pos[i] = pos[p0 + i];
-  }
-  if (threadIdx.x < 32) {
-    const int64_t p = p0 + threadIdx.x;
-    bool begins = false;
-    int64_t e = p;
-    uint32_t x = 0;
-    if (static_cast<int>(threadIdx.x) < span && p < j.tokens) {
-      x = key[p];
-      begins = x < j.vocab && (p == 0 || key[p - 1] != x);
-    }
-    if (begins) {
-      int64_t step = 1;                        // most words are short: look ahead in growing steps
-      while (p + step < j.tokens && key[p + step] == x) step *= 2;
-      const int64_t from = p + step / 2;
-      e = from + run_rank<int64_t>(key + from, min(step - step / 2, j.tokens - from), x, true);
-    }
-    const unsigned all = __ballot_sync(0xffffffffu, begins);
-    if (begins) {
-      const int at = __popc(all & ((1u << threadIdx.x) - 1u));
-      first[at] = p;
-      last[at] = e;
-      word[at] = x;
-    }
-    if (threadIdx.x == 0) words = __popc(all);
-  }
-  __syncthreads();
-  // The rows of word r, loose tokens before whole chunks' sums.
-  struct Rows {
-    int64_t a, head, loose, skip, lo, count;
-  };
-  const auto rows_of = [&](int r) {
-    Rows w;
-    w.a = first[r];
-    const int64_t b = last[r], hi = b / kChunk;
-    w.lo = (w.a + kChunk - 1) / kChunk;
-    const bool whole = w.lo < hi;
-    w.head = whole ? w.lo * kChunk - w.a : b - w.a;
-    w.loose = whole ? w.head + b - hi * kChunk : w.head;
-    w.skip = whole ? hi * kChunk - w.head : w.a;           // from there on the positions behind the chunks
-    w.count = w.loose + (whole ? hi - w.lo : 0);
-    return w;
-  };
-  const auto add_part = [&](Strip<VEC>& s, const Rows& w, int64_t from, int64_t to, int64_t c0) {
-    add_rows<TYPE, VEC, kRowsAhead<TYPE>>(s, j.dy, j.ld_dy, min(to, w.loose) - from, c0, j.n, [&](int64_t i) {
-      const int64_t p = (from + i < w.head ? w.a : w.skip) + from + i;
-      return p - p0 < kPositions ? near_pos[p - p0] : __ldg(pos + p);
-    });
-    const int64_t begin = max(from, w.loose);
-    add_rows<kF32, VEC, kRowsAhead<kF32>>(s, partial, j.n, to - begin, c0, j.n,
-                                          [&](int64_t i) { return static_cast<uint32_t>(w.lo + (begin - w.loose) + i); });
-  };
   const int warp = threadIdx.x >> 5;
-  const int strip0 = static_cast<int>(blockIdx.x % groups) * kBlockStrips, here = min(kBlockStrips, strips - strip0);
-  constexpr int kFewColumns = VEC ? 512 : 128;
-  const int64_t columns = min(static_cast<int64_t>(here) * strip_columns(VEC), j.n - static_cast<int64_t>(strip0) * strip_columns(VEC));
-  const int parts = static_cast<int>((columns + kFewColumns - 1) / kFewColumns);
-  for (int item = warp; item < words * parts; item += kWarps) {
-    const int r = item / parts;
-    const int count = static_cast<int>(min(last[r] - first[r], static_cast<int64_t>(kFewTokens + 1)));
-    if (count <= kFewTokens)
-      few_tokens<TYPE, VEC, ACC, OUT32>(j, near_pos + (first[r] - p0), count, word[r],
-                                        static_cast<int64_t>(strip0) * strip_columns(VEC) + (item - r * parts) * kFewColumns);
-  }
-  for (int item = warp; item < words * here; item += kWarps) {
-    const int r = item / here;
-    if (last[r] - first[r] <= kFewTokens) continue;
-    const Rows w = rows_of(r);
-    if (w.count > kManyRows) continue;
-    const int64_t c0 = static_cast<int64_t>(strip0 + item - r * here) * strip_columns(VEC);
-    OldStrip<VEC> old;
-    old.load(j, word[r], c0);
-    Strip<VEC> s;
-    s.clear();
-    add_part(s, w, 0, w.count, c0);
-    finish_row<VEC>(s, old, j, word[r], c0);
-  }
-  for (int r = 0; r < words; ++r) {
-    if (last[r] - first[r] <= kManyRows) continue;
-    const Rows w = rows_of(r);
-    if (w.count <= kManyRows) continue;        // the same in all threads
-    for (int strip = strip0; strip < strip0 + here; ++strip) {
-      const int64_t c0 = static_cast<int64_t>(strip) * strip_columns(VEC);
+  if (blockIdx.x < heavy_blocks) {
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x / strips) * kPositions;
+    find_words(words, j, key, pos, p0, kPositions, kManyRows + 1);
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % strips) * strip_columns(VEC);
+    for (int r = 0; r < words.count; ++r) {    // in any order: their rows are disjoint
+      const WordRows w(words.first[r], words.last[r]);
+      if (w.count <= kManyRows) continue;      // the same in all threads
       Strip<VEC> s;
       s.clear();
-      add_part(s, w, w.count * warp / kWarps, w.count * (warp + 1) / kWarps, c0);
-      join_parts<VEC>(part, s, j, word[r], c0);
+      add_word<TYPE, VEC>(s, j, words, pos, p0, partial, w, w.count * warp / kWarps, w.count * (warp + 1) / kWarps, c0);
+      join_parts<VEC>(part, s, j, words.word[r], c0);
     }
+    return;
+  }
+  const unsigned block = blockIdx.x - heavy_blocks;
+  const int64_t p0 = static_cast<int64_t>(block / groups) * span;
+  find_words(words, j, key, pos, p0, span, 1);
+  const int strip0 = static_cast<int>(block % groups) * kBlockStrips, here = min(kBlockStrips, strips - strip0);
+  const int64_t c_begin = static_cast<int64_t>(strip0) * strip_columns(VEC);
+  constexpr int kFewColumns = VEC ? 512 : 128;
+  const int64_t columns = min(static_cast<int64_t>(here) * strip_columns(VEC), j.n - c_begin);
+  const int parts = static_cast<int>((columns + kFewColumns - 1) / kFewColumns);
+  const int count = words.count;
+  for (int item = warp; item < count * parts; item += kWarps) {
+    const int r = item / parts;
+    const int64_t tokens = words.last[r] - words.first[r];
+    if (tokens <= kFewTokens)
+      few_tokens<TYPE, VEC, ACC, OUT32>(j, words.pos + (words.first[r] - p0), static_cast<int>(tokens), words.word[r],
+                                        c_begin + (item - r * parts) * kFewColumns);
+  }
+  for (int item = warp; item < count * here; item += kWarps) {
+    const int r = item / here;
+    if (words.last[r] - words.first[r] <= kFewTokens) continue;
+    const WordRows w(words.first[r], words.last[r]);
+    if (w.count > kManyRows) continue;
+    const int64_t c0 = c_begin + static_cast<int64_t>(item - r * here) * strip_columns(VEC);
+    OldStrip<VEC> old;
+    old.load(j, words.word[r], c0);
+    Strip<VEC> s;
+    s.clear();
+    add_word<TYPE, VEC>(s, j, words, pos, p0, partial, w, 0, w.count, c0);
+    finish_row<VEC>(s, old, j, words.word[r], c0);
   }
 }
 
@@ -815,14 +838,16 @@ cudaError_t launch_sums(const EmbeddingBackwardJob& j, const uint32_t* key, cons
   const cudaError_t e = counted(cudaGetLastError());
   if (e != cudaSuccess) return e;
   const int64_t groups = ceil_div(strips, kBlockStrips);
-  const int64_t span = std::max<int64_t>(1, std::min<int64_t>(kMaxRows / 2, j.tokens * groups / (kSms * 16)));
-  const unsigned grid = static_cast<unsigned>(ceil_div(j.tokens, span) * groups), gr = static_cast<unsigned>(groups);
+  const int64_t span = std::max<int64_t>(1, std::min<int64_t>(kMaxRows / 2, j.tokens * groups / (kSms * 8)));
+  const unsigned heavy = static_cast<unsigned>(ceil_div(j.tokens, kPositions) * strips);
+  const unsigned grid = heavy + static_cast<unsigned>(ceil_div(j.tokens, span) * groups);
   const int sp = static_cast<int>(span), st = static_cast<int>(strips);
+  const unsigned gr = static_cast<unsigned>(groups);
   const bool out32 = j.dtable_type == kF32;
-  if (j.accumulate && out32) embedding_touched_kernel<TYPE, VEC, true, true><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr);
-  else if (j.accumulate) embedding_touched_kernel<TYPE, VEC, true, false><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr);
-  else if (out32) embedding_touched_kernel<TYPE, VEC, false, true><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr);
-  else embedding_touched_kernel<TYPE, VEC, false, false><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr);
+  if (j.accumulate && out32) embedding_touched_kernel<TYPE, VEC, true, true><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
+  else if (j.accumulate) embedding_touched_kernel<TYPE, VEC, true, false><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
+  else if (out32) embedding_touched_kernel<TYPE, VEC, false, true><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
+  else embedding_touched_kernel<TYPE, VEC, false, false><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
   return counted(cudaGetLastError());
 }
 
