@@ -106,6 +106,27 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int type, const float
   }
 }
 
+// A kernel that follows another one on the stream and reads what that one wrote
+// may be set up while the other still runs: it is launched by launch_after, and
+// waits here, before its first access to memory, until the other has ended and
+// its writes are visible. (Launched plainly, the second kernel begins about 1 us
+// later.)
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Rows that start at multiples of 8 elements.
 inline bool rows_by_8(const void* p, int64_t ld, int type) {
   return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(8 * elem_bytes(type)) == 0 && ld % 8 == 0;

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t group = static_cast<int64_t>(blockIdx.y) * (kRun * kFan);
   const int count = static_cast<int>(min(static_cast<int64_t>(kRun * kFan), tokens - group));
   const int nruns = (count + kRun - 1) / kRun;
+  wait_for_previous();
 #pragma unroll 8
   for (int i = threadIdx.x; i < nruns * (kRun / 4); i += kJoinThreads) {
     uint4 k = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kThreads)
                                int64_t tokens, int64_t run, int lanes) {
   const int64_t items = kThreads / lanes;
   const int lane = threadIdx.x & (lanes - 1);
+  wait_for_previous();
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * items; base < tokens;
        base += static_cast<int64_t>(gridDim.x) * items) {
     const int64_t e = base + threadIdx.x / lanes;
@@ -459,6 +461,7 @@ template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4)
     embedding_chunks_kernel(const __grid_constant__ EmbeddingBackwardJob j, const uint32_t* key, const uint32_t* pos,
                             float* partial, int strips, unsigned chunk_blocks, int rows) {
+  wait_for_previous();
   if (blockIdx.x >= chunk_blocks) {
     __shared__ int64_t stretch[2];
     __shared__ int has[kMaxRows];
@@ -770,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   __shared__ Words words;
   __shared__ float part[kWarps][strip_columns(VEC)];
   const int warp = threadIdx.x >> 5;
+  wait_for_previous();
   if (blockIdx.x < heavy_blocks) {
     const int64_t p0 = static_cast<int64_t>(blockIdx.x / strips) * kPositions;
     find_words(words, j, key, pos, p0, kPositions, kManyRows + 1);
@@ -833,9 +837,10 @@ cudaError_t launch_sums(const EmbeddingBackwardJob& j, const uint32_t* key, cons
   const int64_t chunk_blocks = ceil_div(j.tokens / kChunk * strips, kWarps);
   const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(kMaxRows, j.vocab / (kSms * 8)));
   const int64_t zero_blocks = j.accumulate ? 0 : ceil_div(j.vocab, rows);
-  embedding_chunks_kernel<TYPE, VEC><<<static_cast<unsigned>(chunk_blocks + zero_blocks), kThreads, 0, s>>>(
-      j, key, pos, partial, static_cast<int>(strips), static_cast<unsigned>(chunk_blocks), static_cast<int>(rows));
-  const cudaError_t e = counted(cudaGetLastError());
+  const cudaError_t e = counted(launch_after(embedding_chunks_kernel<TYPE, VEC>,
+                                             static_cast<unsigned>(chunk_blocks + zero_blocks), kThreads, 0, s, j, key, pos,
+                                             partial, static_cast<int>(strips), static_cast<unsigned>(chunk_blocks),
+                                             static_cast<int>(rows)));
   if (e != cudaSuccess) return e;
   const int64_t groups = ceil_div(strips, kBlockStrips);
   const int64_t span = std::max<int64_t>(1, std::min<int64_t>(kMaxRows / 2, j.tokens * groups / (kSms * 8)));
@@ -844,11 +849,13 @@ cudaError_t launch_sums(const EmbeddingBackwardJob& j, const uint32_t* key, cons
   const int sp = static_cast<int>(span), st = static_cast<int>(strips);
   const unsigned gr = static_cast<unsigned>(groups);
   const bool out32 = j.dtable_type == kF32;
-  if (j.accumulate && out32) embedding_touched_kernel<TYPE, VEC, true, true><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
-  else if (j.accumulate) embedding_touched_kernel<TYPE, VEC, true, false><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
-  else if (out32) embedding_touched_kernel<TYPE, VEC, false, true><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
-  else embedding_touched_kernel<TYPE, VEC, false, false><<<grid, kThreads, 0, s>>>(j, key, pos, partial, sp, st, gr, heavy);
-  return counted(cudaGetLastError());
+  const auto launch = [&](auto kernel) {
+    return counted(launch_after(kernel, grid, kThreads, 0, s, j, key, pos, partial, sp, st, gr, heavy));
+  };
+  if (j.accumulate && out32) return launch(embedding_touched_kernel<TYPE, VEC, true, true>);
+  if (j.accumulate) return launch(embedding_touched_kernel<TYPE, VEC, true, false>);
+  if (out32) return launch(embedding_touched_kernel<TYPE, VEC, false, true>);
+  return launch(embedding_touched_kernel<TYPE, VEC, false, false>);
 }
 
 // The join's shared memory is asked for once per device.
@@ -935,17 +942,17 @@ cudaError_t launch_embedding_backward(const EmbeddingBackwardJob& j, void* ws, c
         for (int64_t g = 0; g < groups; g += 65535) {
           const int64_t skip = g * kRun * kFan;
           const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min<int64_t>(65535, groups - g)));
-          embedding_join_first_kernel<<<grid, kJoinThreads, bytes, s>>>(key + skip, pos + skip, key2 + skip, pos2 + skip,
-                                                                       j.tokens - skip);
-          if ((e = counted(cudaGetLastError())) != cudaSuccess) return e;
+          e = counted(launch_after(embedding_join_first_kernel, grid, kJoinThreads, bytes, s, key + skip, pos + skip,
+                                   key2 + skip, pos2 + skip, j.tokens - skip));
+          if (e != cudaSuccess) return e;
         }
       } else {
         int lanes = 1;
         while (lanes < 32 && lanes < ceil_div(j.tokens, run)) lanes *= 2;
         const int64_t blocks = std::min<int64_t>(ceil_div(j.tokens, kThreads / lanes), kSms * 32);
-        embedding_join_runs_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(key, pos, key2, pos2, j.tokens,
-                                                                                     run, lanes);
-        if ((e = counted(cudaGetLastError())) != cudaSuccess) return e;
+        e = counted(launch_after(embedding_join_runs_kernel, static_cast<unsigned>(blocks), kThreads, 0, s, key, pos, key2,
+                                 pos2, j.tokens, run, lanes));
+        if (e != cudaSuccess) return e;
       }
       std::swap(key, key2);
       std::swap(pos, pos2);

@@ -155,6 +155,7 @@ __device__ __forceinline__ float total_norm(const double* partial, int64_t count
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* partial, int64_t count, float* norm) {
+  wait_for_previous();
   const float v = total_norm(partial, count);
   if (threadIdx.x == 0) *norm = v;
 }
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kThreads)
     grad_clip_kernel(const __grid_constant__ Spans<N> b, const double* partial, int64_t partials, float max_norm,
                      float* norm, int write_norm) {
   float v_norm;
+  wait_for_previous();
   if (partial != nullptr) {
     v_norm = total_norm(partial, partials);
     if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v_norm;
@@ -223,6 +225,12 @@ cudaError_t each_launch(const intlora_grad_job* jobs, int32_t count, F f) {
   }
   return cudaSuccess;
 }
+template <int N>
+cudaError_t clip_after(const Spans<N>& b, int64_t blocks, const void* ws, int64_t partials, float max_norm, float* norm,
+                       int write, cudaStream_t s) {
+  return counted(launch_after(grad_clip_kernel<N>, static_cast<unsigned>(blocks), kThreads, 0, s, b,
+                              static_cast<const double*>(ws), partials, max_norm, norm, write));
+}
 template <typename F>
 cudaError_t each_launch(const intlora_grad_job* jobs, int32_t count, F f) {
   return count <= kFewSpans ? each_launch<kFewSpans>(jobs, count, f) : each_launch<kMaxSpans>(jobs, count, f);
@@ -255,18 +263,16 @@ cudaError_t launch_grad_squares(const intlora_grad_job* jobs, int32_t count, voi
 }
 
 cudaError_t launch_grad_norm_finish(int64_t partials, const void* ws, float* norm, cudaStream_t s) {
-  grad_norm_finish_kernel<<<1, kThreads, 0, s>>>(static_cast<const double*>(ws), partials, norm);
-  return counted(cudaGetLastError());
+  return counted(launch_after(grad_norm_finish_kernel, 1, kThreads, 0, s, static_cast<const double*>(ws), partials, norm));
 }
 
 cudaError_t launch_grad_clip(const intlora_grad_job* jobs, int32_t count, float max_norm, const void* ws,
                              int64_t partials, float* norm, cudaStream_t s) {
   int write = 1;                               // the first launch writes the norm
   return each_launch(jobs, count, [&](const auto& b, int64_t blocks) {
-    grad_clip_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, static_cast<const double*>(ws), partials,
-                                                                       max_norm, norm, write);
+    const cudaError_t launched = clip_after(b, blocks, ws, partials, max_norm, norm, write, s);
     write = 0;
-    return counted(cudaGetLastError());
+    return launched;
   });
 }
 
@@ -280,9 +286,7 @@ cudaError_t launch_clip_grad_norm(const intlora_grad_job* jobs, int32_t count, f
     grad_squares_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, static_cast<double*>(ws));
     const cudaError_t e = counted(cudaGetLastError());
     if (e != cudaSuccess) return e;
-    grad_clip_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(b, static_cast<const double*>(ws), partials,
-                                                                       max_norm, norm, 1);
-    return counted(cudaGetLastError());
+    return clip_after(b, blocks, ws, partials, max_norm, norm, 1, s);
   });
 }
 

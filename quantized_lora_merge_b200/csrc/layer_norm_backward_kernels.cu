@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
+  wait_for_previous();
   if (c < 2 * n) {
 #pragma unroll 8
     for (int64_t p = warp; p < blocks; p += kReduceWarps) s += partial[p * 2 * n + c];
@@ -377,9 +378,8 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardJob& j, void* ws, 
     if (e != cudaSuccess) return e;
   }
   if (!sums) return cudaSuccess;
-  layer_norm_reduce_kernel<<<static_cast<unsigned>((2 * j.n + 31) / 32), 32 * kReduceWarps, 0, s>>>(
-      partial, b.blocks, j.n, j.dweight, j.dbias, j.accumulate);
-  return counted(cudaGetLastError());
+  return counted(launch_after(layer_norm_reduce_kernel, static_cast<unsigned>((2 * j.n + 31) / 32), 32 * kReduceWarps, 0, s,
+                              partial, b.blocks, j.n, j.dweight, j.dbias, j.accumulate));
 }
 
 }  // namespace intlora
