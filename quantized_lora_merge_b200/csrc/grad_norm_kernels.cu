@@ -53,6 +53,12 @@ __device__ __forceinline__ double square_sum(const float (&v)[kPerThread]) {
   for (int i = 0; i < kPerThread; ++i) s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
   const float f = (s[0] + s[1]) + (s[2] + s[3]);
   if (f > 0x1p-90f && f < 0x1p126f) return f;
+  if (f == 0.0f) {                             // nothing but zeros (a factor's first step), or squares too small
+    uint32_t any = 0u;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) any |= __float_as_uint(v[i]) << 1;
+    if (any == 0u) return 0.0;
+  }
   double d = 0.0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) d = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), d);
