@@ -1087,7 +1087,7 @@ const char* intlora_status_string(int status) {
 
 const char* intlora_last_error(void) { return g_last_error; }
 
-int intlora_version(void) { return 200; }   // 0.2.0: descriptors gained trailing fields
+int intlora_version(void) { return 300; }   // 0.3.0: layer norm, embedding, gradient clipping
 
 uint64_t intlora_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
