@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(kBlock, 1)
   const auto fetch = [&](int slot, int64_t which) {
     if (which < j.tokens && !idle) {
       const uint32_t stage = mine + slot * r.stage_bytes;
-      fetch_row<kBytes<TX>, F>(stage, next_x, which == 0, n, t, T);
-      fetch_row<kBytes<TY>, F>(stage + r.second, next_dy, which == 0, n, t, T);
+      fetch_row<kBytes<TX>, F>(stage, next_x, j.x, n, t, T);
+      fetch_row<kBytes<TY>, F>(stage + r.second, next_dy, j.dy, n, t, T);
     }
     copy_commit();
     next_x += x_step;

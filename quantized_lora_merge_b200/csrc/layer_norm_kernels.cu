@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kBlock, 1)
   const char* here = next;
   char* y = static_cast<char*>(row_ptr(j.y, row, j.ld_y, j.y_type));
   const auto fetch = [&](int slot, int64_t which) {
-    if (which < j.tokens && !idle) fetch_row<kBytes<TX>, F>(mine + slot * r.stage_bytes, next, which == 0, n, t, T);
+    if (which < j.tokens && !idle) fetch_row<kBytes<TX>, F>(mine + slot * r.stage_bytes, next, j.x, n, t, T);
     copy_commit();
     next += x_step;
   };

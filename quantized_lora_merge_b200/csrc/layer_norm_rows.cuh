@@ -381,10 +381,10 @@ __device__ __forceinline__ void copy_wait(int newer) {
   }
 }
 
-// Starts the copy of a row that begins at src into its place in the ring.
-// first_row: nothing before src belongs to the tensor.
+// Starts the copy of a row that begins at src into its place in the ring. Nothing
+// before base belongs to the tensor.
 template <int ES, typename F>
-__device__ __forceinline__ void fetch_row(uint32_t stage, const char* src, bool first_row, int n, int t, int T) {
+__device__ __forceinline__ void fetch_row(uint32_t stage, const char* src, const void* base, int n, int t, int T) {
   constexpr int es = ES;
   if (F::VEC) {
     const int at = t / F::L * F::V * F::kCols * es + (t & (F::L - 1)) * 16;
@@ -396,16 +396,19 @@ __device__ __forceinline__ void fetch_row(uint32_t stage, const char* src, bool 
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15u);
     const int end = shift + n * es;            // of the row, from its first granule on
     const char* from = src - shift;
-    const bool cut = first_row && shift != 0;  // the first granule begins before the tensor
+    // the first granule begins before the tensor: the first row, or one of the
+    // first rows where several begin in one granule
+    const bool cut = from < static_cast<const char*>(base);
     const int whole = end / 16 * 16;
 #pragma unroll 1
     for (int g = (t == 0 && cut ? T : t) * 16; g < whole; g += T * 16) copy16(stage + g, from + g);
     if (t == 0 && cut) {
-      for (int b = shift; b < min(end, 16); b += es) {
+      for (int b = shift; b < 16; b += es) {   // zeros where the row ends in the granule
         if (es == 4)
-          *reinterpret_cast<uint32_t*>(smem() + stage + b) = *reinterpret_cast<const uint32_t*>(from + b);
+          *reinterpret_cast<uint32_t*>(smem() + stage + b) = b < end ? *reinterpret_cast<const uint32_t*>(from + b) : 0u;
         else
-          *reinterpret_cast<uint16_t*>(smem() + stage + b) = *reinterpret_cast<const uint16_t*>(from + b);
+          *reinterpret_cast<uint16_t*>(smem() + stage + b) =
+              b < end ? *reinterpret_cast<const uint16_t*>(from + b) : uint16_t{0};
       }
     }
     // the granule in which the row ends, filled up with zeros, and one of zeros

@@ -116,6 +116,22 @@ def test_strides_and_alignment_leave_what_lies_between(n, pad, shift):
         assert bool((buffer[keep] == GUARD).all())
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 7])
+@pytest.mark.parametrize("shift", [0, 1, 3, 6])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_rows_of_which_several_share_sixteen_bytes(n, shift, dtype):
+    """Rows shorter than an access, from a base inside one, more of them than
+    blocks, so that every place in the ring is used again."""
+    tokens = 6000
+    x, w, b, r = _inputs(tokens, n, dtype, F32, seed=n, shift=shift)
+    buf, y, mean, rstd = _forward(x, w, b, dtype, shift=shift)
+    _check_forward(x, w, b, y, mean, rstd)
+    _, dy = _strided(tokens, n, dtype, 0, shift)
+    dy.copy_(0.05 * r(tokens, n))
+    _, dx, dw, db = _backward(dy, x, w, mean, rstd, dtype, shift=shift)
+    _check_backward(dy, x, w, mean, rstd, dx, dw, db)
+
+
 @pytest.mark.parametrize("n", [264, 4096])
 def test_parts_left_out(n):
     tokens = 200
