@@ -89,8 +89,18 @@ __global__ void __launch_bounds__(kBlock, 1)
         read_chunk<TX, F>(sx, j.x_type, c, k, px[0], px[1]);
         read_chunk<TY, F>(sy, j.dy_type, c, k, py[0], py[1]);
         param_chunk<F>(r.params, c, k, pw[0], pw[1]);
-        px[0] = (px[0] + m) * scale;
-        px[1] = (px[1] + m) * scale;
+        // columns past n: xh is zero like x and dy; -mean rstd may be beyond fp32,
+        // and NaN in the row's sums (up to 3 % of the time; a second sum for such
+        // rows alone spills, and takes more)
+        if constexpr (F::VEC) {
+          const F2 mk = c.has(k, 0) ? m : f2(0.0f);
+          px[0] = (px[0] + mk) * scale;
+          px[1] = (px[1] + mk) * scale;
+        } else {
+          const float m1 = split(m).x;
+          px[0] = (px[0] + f2(c.has(k, 0) ? m1 : 0.0f, c.has(k, 1) ? m1 : 0.0f)) * scale;
+          px[1] = (px[1] + f2(c.has(k, 2) ? m1 : 0.0f, c.has(k, 3) ? m1 : 0.0f)) * scale;
+        }
       };
       if (live) {
 #pragma unroll
@@ -99,7 +109,6 @@ __global__ void __launch_bounds__(kBlock, 1)
           F2* pg = g + (kHold ? 2 * k : 0);
           F2 dy[2], w[2];
           load(k, px, dy, w);
-          // columns past n: dy is zero there, and xh is finite (x = 0)
           pg[0] = dy[0] * w[0];
           pg[1] = dy[1] * w[1];
           s0 = s0 + (pg[0] + pg[1]);

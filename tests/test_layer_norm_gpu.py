@@ -132,6 +132,24 @@ def test_rows_of_which_several_share_sixteen_bytes(n, shift, dtype):
     _check_backward(dy, x, w, mean, rstd, dx, dw, db)
 
 
+# more rows than the kernel without a ring takes; half-warp forms of every V
+MANY_ROWS = [(1300, 33), (1300, 101), (1300, 255), (1300, 1001), (1300, 5003), (1200, 9001)] + [
+    (700, n) for n in (72, 136, 192, 200, 320, 384, 512, 640, 1280, 2048, 16384)]
+
+
+@pytest.mark.parametrize("tokens,n", MANY_ROWS)
+@pytest.mark.parametrize("x_dtype,p_dtype,pad,shift", [(F32, BF16, 0, 0), (BF16, F32, 0, 0), (F16, F16, 8, 0),
+                                                       (BF16, F32, 3, 5), (F32, F32, 1, 1)])
+def test_many_rows(tokens, n, x_dtype, p_dtype, pad, shift):
+    x, w, b, r = _inputs(tokens, n, x_dtype, p_dtype, seed=n, pad=pad, shift=shift)
+    _, y, mean, rstd = _forward(x, w, b, x_dtype, pad=pad, shift=shift)
+    _check_forward(x, w, b, y, mean, rstd)
+    _, dy = _strided(tokens, n, x_dtype, pad, shift)
+    dy.copy_(0.05 * r(tokens, n))
+    _, dx, dw, db = _backward(dy, x, w, mean, rstd, x_dtype, pad=pad, shift=shift)
+    _check_backward(dy, x, w, mean, rstd, dx, dw, db)
+
+
 @pytest.mark.parametrize("n", [264, 4096])
 def test_parts_left_out(n):
     tokens = 200
@@ -191,6 +209,20 @@ def test_offsets_constants_and_values_that_are_not_finite(n):
     good = [i for i in range(9) if i not in bad]
     assert bool(torch.isnan(y[bad]).all())
     _check_forward(x[good], w, b, y[good], mean[good], rstd[good])
+
+
+@pytest.mark.parametrize("n", [3, 20, 33, 40, 264, 520, 1001, 4104, 5003, 9000])
+def test_gradient_of_huge_constant_rows(n):
+    """xh is zero, although mean rstd is beyond fp32: no column past n may reach
+    the sums. rstd is what eps = 1e-5 gives."""
+    tokens = 300
+    x, w, _, r = _inputs(tokens, n, F32, F32, seed=n)
+    x[::2] = 2.0 ** 120
+    mean, rstd = x.double().mean(1).float(), torch.full((tokens,), 316.227766, device=dev())
+    mean[::2] = 2.0 ** 120
+    dy = 0.05 * r(tokens, n)
+    _, dx, dw, db = _backward(dy, x, w, mean, rstd, F32)
+    _check_backward(dy, x, w, mean, rstd, dx, dw, db)
 
 
 def test_jobs_of_one_call_and_streams():
