@@ -493,8 +493,9 @@ intlora_status intlora_train_backward_batched(const intlora_train_backward_job* 
  * weight, bias (both param_type, [n]) may be NULL (1 and 0); mean and rstd
  * (fp32 [tokens], what the backward takes) may be NULL. n >= 1, eps finite and
  * >= 0; a constant row with eps = 0 gives what 0 / 0 gives. One launch a job;
- * the jobs of a call do not depend on one another. Asynchronous on `stream`;
- * no workspace. */
+ * the jobs of a call do not depend on one another. y may be x itself (one type
+ * and stride); no other overlap of what a job writes with what it reads.
+ * Asynchronous on `stream`; no workspace. */
 typedef struct intlora_layer_norm_job {
     const void* x;            /* tokens x n */
     const void* weight;
@@ -516,7 +517,8 @@ intlora_status intlora_layer_norm_batched(const intlora_layer_norm_job* jobs, in
  *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy   (fp32 [n])
  * mean and rstd are those of the forward. dx, dweight and dbias may each be
  * NULL (not computed). dweight and dbias are overwritten, or added to with
- * accumulate != 0; tokens = 0 gives zero sums. Workspace (256-byte aligned):
+ * accumulate != 0; tokens = 0 gives zero sums. dx may be dy or x itself (one
+ * type and stride). Workspace (256-byte aligned):
  * one row of partial sums per thread block, for jobs with dweight or dbias. */
 typedef struct intlora_layer_norm_backward_job {
     const void* dy;           /* tokens x n */

@@ -360,14 +360,14 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardJob& j, void* ws, 
   const bool sums = j.dweight != nullptr || j.dbias != nullptr;
   float* partial = sums ? static_cast<float*>(ws) : nullptr;
   if (b.wide) {
-    if (j.dx != nullptr && j.tokens > 0) {
-      layer_norm_backward_wide_kernel<<<grid_of(j.tokens, 1 << 20), kWideThreads, 0, s>>>(j);
+    if (sums) {                                // first: dx may take the place of dy or x
+      const dim3 grid(static_cast<unsigned>((j.n + kColThreads - 1) / kColThreads), static_cast<unsigned>(b.blocks));
+      layer_norm_columns_kernel<<<grid, kColThreads, 0, s>>>(j, partial);
       const cudaError_t e = counted(cudaGetLastError());
       if (e != cudaSuccess) return e;
     }
-    if (sums) {
-      const dim3 grid(static_cast<unsigned>((j.n + kColThreads - 1) / kColThreads), static_cast<unsigned>(b.blocks));
-      layer_norm_columns_kernel<<<grid, kColThreads, 0, s>>>(j, partial);
+    if (j.dx != nullptr && j.tokens > 0) {
+      layer_norm_backward_wide_kernel<<<grid_of(j.tokens, 1 << 20), kWideThreads, 0, s>>>(j);
       const cudaError_t e = counted(cudaGetLastError());
       if (e != cudaSuccess) return e;
     }

@@ -150,6 +150,27 @@ def test_many_rows(tokens, n, x_dtype, p_dtype, pad, shift):
     _check_backward(dy, x, w, mean, rstd, dx, dw, db)
 
 
+@pytest.mark.parametrize("tokens,n", [(5, 264), (1300, 8), (1300, 33), (300, 320), (1300, 1001), (300, 4096), (200, 9000),
+                                      (20, 40000)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_in_place(tokens, n, dtype):
+    """y in the place of x, dx in that of dy or of x: the bits of separate tensors."""
+    x, w, b, r = _inputs(tokens, n, dtype, F32, seed=n)
+    _, y, mean, rstd = _forward(x, w, b, dtype)
+    dy = (0.05 * r(tokens, n)).to(dtype)
+    _, dx, dw, db = _backward(dy, x, w, mean, rstd, dtype)
+    there = x.clone()
+    B.intlora_layer_norm_batched([B.LayerNormJob(there, w, b, there)])
+    assert torch.equal(there, y)
+    for over_x in (False, True):
+        xc, dyc = x.clone(), dy.clone()
+        dw2, db2 = torch.empty(n, device=dev()), torch.empty(n, device=dev())
+        jobs = [B.LayerNormBackwardJob(dyc, xc, w, mean, rstd, xc if over_x else dyc, dw2, db2)]
+        ws = torch.empty(B.intlora_layer_norm_backward_workspace_size(jobs), dtype=torch.uint8, device=dev())
+        B.intlora_layer_norm_backward_batched(jobs, ws)
+        assert torch.equal(xc if over_x else dyc, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+
+
 @pytest.mark.parametrize("n", [264, 4096])
 def test_parts_left_out(n):
     tokens = 200
