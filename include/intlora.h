@@ -541,8 +541,8 @@ intlora_status intlora_layer_norm_backward_batched(const intlora_layer_norm_back
                                                    int32_t count, void* ws, size_t ws_bytes,
                                                    void* stream);
 
-/* Embedding lookup: y[t] = scale * table[ids[t]]. ids: int32 or int64
- * (id_bytes 4 or 8). An id outside [0, vocab) reads nothing: its row of y is
+/* Embedding lookup: y[t] = scale * table[ids[t]], scale finite. ids: int32 or
+ * int64 (id_bytes 4 or 8). An id outside [0, vocab) reads nothing: its row of y is
  * zero, and if `invalid` (a device int32, may be NULL) is given, the number of
  * such ids is added to it. Asynchronous on `stream`; no workspace. */
 typedef struct intlora_embedding_job {

@@ -129,6 +129,7 @@ intlora_status check_emb(const intlora_embedding_job& j, int k) {
     return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: types must be INTLORA_TYPE_*", what, k);
   if (j.id_bytes != 4 && j.id_bytes != 8)
     return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: id_bytes must be 4 or 8", what, k);
+  if (!std::isfinite(j.scale)) return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: scale must be finite", what, k);
   if ((s = check_rows(what, k, "table", j.vocab, j.n, j.ld_table)) != INTLORA_OK) return s;
   if ((s = check_rows(what, k, "y", j.tokens, j.n, j.ld_y)) != INTLORA_OK) return s;
   if (j.tokens == 0) return INTLORA_OK;
@@ -150,6 +151,7 @@ intlora_status check_embb(const intlora_embedding_backward_job& j, int k) {
     return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: types must be INTLORA_TYPE_*", what, k);
   if (j.id_bytes != 4 && j.id_bytes != 8)
     return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: id_bytes must be 4 or 8", what, k);
+  if (!std::isfinite(j.scale)) return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: scale must be finite", what, k);
   if ((s = check_rows(what, k, "dtable", j.vocab, j.n, j.ld_dtable)) != INTLORA_OK) return s;
   if ((s = check_rows(what, k, "dy", j.tokens, j.n, j.ld_dy)) != INTLORA_OK) return s;
   if (j.dtable == nullptr) return fail(INTLORA_ERR_INVALID_ARG, "%s job %d: dtable is required", what, k);

@@ -95,6 +95,16 @@ def test_embedding_backward_rejects(lib, field, value, needle):
     assert needle in lib.intlora_last_error().decode()
 
 
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_embedding_rejects_a_scale_that_makes_missing_rows_nan(lib, scale):
+    jobs = _job(B.intlora_embedding_job, EMB, scale=scale)
+    assert lib.intlora_embedding_batched(jobs, 1, None) == 1
+    assert "scale" in lib.intlora_last_error().decode()
+    jobs = _job(B.intlora_embedding_backward_job, EMBB, scale=scale)
+    assert lib.intlora_embedding_backward_batched(jobs, 1, FAKE, 1 << 30, None) == 1
+    assert "scale" in lib.intlora_last_error().decode()
+
+
 def test_embedding_backward_workspace_checked(lib):
     jobs = _job(B.intlora_embedding_backward_job, EMBB, tokens=1000)
     need = lib.intlora_embedding_backward_workspace_size(jobs, 1)
