@@ -583,16 +583,25 @@ def _device_index(jobs) -> int:
     return indices.pop()
 
 
-def _here(jobs) -> None:
-    """The library launches on the current device: the tensors must be there."""
+def _here(jobs, *others) -> None:
+    """The library launches on the current device: the tensors must be there,
+    the workspace and the norm (`others`, None left out) too."""
     import torch
     if isinstance(jobs, Descriptors):
         index = jobs.device_index
     else:
         index = _device_index(jobs) if len(jobs) else None
-    if index is not None and index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{index}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    found = set() if index is None else {index}
+    for t in others:
+        if t is None:
+            continue
+        if t.device.type != "cuda" or not t.is_contiguous():
+            raise ValueError("workspace and norm must be contiguous and on a CUDA device, got "
+                             f"{t.device}")
+        found.add(t.device.index)
+    if found and found != {torch.cuda.current_device()}:
+        raise ValueError(f"tensors are on cuda:{', cuda:'.join(map(str, sorted(found)))}, the "
+                         f"current device is cuda:{torch.cuda.current_device()}")
 
 
 def _norm_scalar(norm) -> int:
@@ -818,7 +827,7 @@ def intlora_layer_norm_backward_workspace_size(jobs: Sequence[LayerNormBackwardJ
 def intlora_layer_norm_backward_batched(jobs: Sequence[LayerNormBackwardJob], ws=None,
                                         stream=None) -> None:
     arr = _array(intlora_layer_norm_backward_job, jobs)
-    _here(jobs)
+    _here(jobs, ws)
     p, nb = _ws(ws)
     _check(lib().intlora_layer_norm_backward_batched(arr, len(jobs), p, nb, _stream(stream)))
 
@@ -837,7 +846,7 @@ def intlora_embedding_backward_workspace_size(jobs: Sequence[EmbeddingBackwardJo
 def intlora_embedding_backward_batched(jobs: Sequence[EmbeddingBackwardJob], ws=None,
                                        stream=None) -> None:
     arr = _array(intlora_embedding_backward_job, jobs)
-    _here(jobs)
+    _here(jobs, ws)
     p, nb = _ws(ws)
     _check(lib().intlora_embedding_backward_batched(arr, len(jobs), p, nb, _stream(stream)))
 
@@ -849,7 +858,7 @@ def intlora_grad_norm_workspace_size(jobs: Sequence[GradJob]) -> int:
 def intlora_grad_norm_batched(jobs: Sequence[GradJob], norm, ws=None, stream=None) -> None:
     """norm (fp32, one element) = sqrt(sum of g^2 over all jobs)."""
     arr = _array(intlora_grad_job, jobs)
-    _here(jobs)
+    _here(jobs, ws, norm)
     p, nb = _ws(ws)
     _check(lib().intlora_grad_norm_batched(arr, len(jobs), _norm_scalar(norm), p, nb,
                                            _stream(stream)))
@@ -858,7 +867,7 @@ def intlora_grad_norm_batched(jobs: Sequence[GradJob], norm, ws=None, stream=Non
 def intlora_grad_clip_batched(jobs: Sequence[GradJob], max_norm: float, norm, stream=None) -> None:
     """g *= min(1, max_norm / (norm + 1e-6)) in place, norm as given."""
     arr = _array(intlora_grad_job, jobs)
-    _here(jobs)
+    _here(jobs, norm)
     _check(lib().intlora_grad_clip_batched(arr, len(jobs), max_norm, _norm_scalar(norm),
                                            _stream(stream)))
 
@@ -867,7 +876,7 @@ def intlora_clip_grad_norm_batched(jobs: Sequence[GradJob], max_norm: float, nor
                                    stream=None) -> None:
     """Both: norm is written, and the gradients are clipped by it in place."""
     arr = _array(intlora_grad_job, jobs)
-    _here(jobs)
+    _here(jobs, ws, norm)
     p, nb = _ws(ws)
     _check(lib().intlora_clip_grad_norm_batched(arr, len(jobs), max_norm, _norm_scalar(norm), p, nb,
                                                 _stream(stream)))

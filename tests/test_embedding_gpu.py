@@ -142,6 +142,36 @@ def test_gradient_widths(tokens, n, vocab, accumulate):
     _check_backward(dy, ids, vocab, dtable, 0.5, old=old)
 
 
+@pytest.mark.parametrize("tokens,n,vocab", [(700, 4100, 9), (600, 1001, 5), (600, 8200, 3), (900, 1, 2), (513, 20008, 200),
+                                            (1500, 129, 70)])
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_widths_of_sorted_texts(tokens, n, vocab, dtype, accumulate):
+    g = _gen(n)
+    _, dy = _rows(tokens, n, dtype, g)
+    ids = torch.randint(0, vocab, (tokens,), device=dev(), generator=g)
+    old = _rows(vocab, n, F32, g)[1] if accumulate else None
+    dtable, _ = _backward(dy, ids, vocab, 0.5, old=old)
+    _check_backward(dy, ids, vocab, dtable, 0.5, old=old)
+
+
+@pytest.mark.parametrize("counts", [[1] * 120 + [600, 1, 16, 17, 9, 8, 300], [127, 1, 700, 31, 33, 64, 65, 7],
+                                    [96, 31, 2, 513, 128, 128, 129, 40], [2000], [5, 640, 3, 544, 4]])
+@pytest.mark.parametrize("n", [24, 264, 301, 2056])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_of_words_across_windows(counts, n, accumulate):
+    """Words of every frequency that begin and end at, before and behind the
+    borders of 32 and of 128 sorted positions."""
+    g = _gen(n)
+    ids = torch.repeat_interleave(torch.arange(len(counts), device=dev()), torch.tensor(counts, device=dev()))
+    ids = ids[torch.randperm(ids.numel(), device=dev(), generator=g)]
+    vocab = len(counts) + 3
+    _, dy = _rows(ids.numel(), n, BF16, g)
+    old = _rows(vocab, n, F32, g)[1] if accumulate else None
+    dtable, _ = _backward(dy, ids, vocab, 1.0, old=old)
+    _check_backward(dy, ids, vocab, dtable, 1.0, old=old)
+
+
 @pytest.mark.parametrize("dy_dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (16, 8), (1, 3)])

@@ -187,6 +187,36 @@ def test_binding_refuses_what_it_cannot_describe():
     assert B._matrix("x", torch.zeros(1, 16).expand(1, 16)) == 16
 
 
+def test_binding_refuses_workspaces_and_norms_elsewhere(monkeypatch):
+    class On:
+        def __init__(self, device, contiguous=True):
+            self.device, self.contiguous = torch.device(device), contiguous
+
+        def is_contiguous(self):
+            return self.contiguous
+
+    class Job:
+        def device(self):
+            return torch.device("cuda:0")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    B._here([Job()], On("cuda:0"), None)
+    B._here([], None)
+    for jobs, other, needle in (([Job()], On("cpu"), "CUDA"), ([Job()], On("cuda:1"), "cuda:0, cuda:1"),
+                                ([], On("cuda:1"), "cuda:1"), ([Job()], On("cuda:0", False), "contiguous")):
+        with pytest.raises(ValueError, match=needle):
+            B._here(jobs, other)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.intlora_layer_norm_backward_batched([], torch.empty(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="CUDA"):
+        B.intlora_embedding_backward_batched([], torch.empty(256, dtype=torch.uint8))
+    with pytest.raises((TypeError, ValueError), match="CUDA"):
+        B.intlora_clip_grad_norm_batched([], 1.0, torch.zeros(1), torch.empty(256, dtype=torch.uint8))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        B._here([Job()])
+
+
 def test_header_accepts_the_descriptors_in_c(tmp_path):
     import shutil
     import subprocess
