@@ -479,9 +479,9 @@ intlora_status intlora_train_backward_batched(const intlora_train_backward_job* 
  * Elements are fp32, bf16 or fp16 (INTLORA_TYPE_*), each tensor with a type of
  * its own; arithmetic, statistics and sums are fp32 or wider and every output
  * is rounded once, to nearest, ties to even. Matrices are row-major with a row
- * stride ld in elements (>= n), any alignment of whole elements; rows at
- * 16-byte boundaries with n % 8 == 0 take 16-byte accesses, others single
- * elements. Results do not depend on the order in which blocks run.
+ * stride ld in elements (>= n), any alignment of whole elements; rows that start
+ * and end at 16-byte boundaries (layer norm) or at multiples of 8 elements
+ * (embedding) take wide accesses, others single elements. Results do not depend on the order in which blocks run.
  * tokens, n and vocab < 2^31; every rows * ld at most 2^40.
  * ------------------------------------------------------------------------ */
 #define INTLORA_TYPE_F32 0

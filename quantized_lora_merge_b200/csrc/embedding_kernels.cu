@@ -3,8 +3,8 @@
 //   forward   y_t = scale E[id_t]
 //   backward  dE_v = scale sum_{t: id_t = v, v != padding} dy_t
 //
-// Both are bound by memory. The forward gathers rows with 16-byte accesses,
-// four rows in flight a thread.
+// Both are bound by memory. The forward gathers rows with 16- or 32-byte
+// accesses, a thread's next rows in flight while it writes the last ones.
 //
 // The backward sorts the token positions by id, so that every table row has one
 // owner that adds its tokens in a fixed order: no atomics on floats, the same
