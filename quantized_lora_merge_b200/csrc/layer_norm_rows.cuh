@@ -486,7 +486,7 @@ inline bool place_ring(const RowWant& q, RowShape* r) {
 // where a round is a row for every team: a row costs a thread the issue slots of
 // its V chunks and of about 8 more (sums across threads, root, addresses), and
 // the wait of a chain as long as V and about 12 more. Measured, us:
-//   forward   16384 x 320 fp16    V = 1, 3, 8, 16: 22.7, 8.5, 13.3, 19.9
+//   forward   16384 x 320 fp16    V = 1, 3, 8, 16: 22.7, 8.5, 13.3, 19.9; half a warp V = 5: 6.8
 //             8192 x 4096 bf16    V = 1, 4, 8, 16: 159, 44, 34, 28.5
 //   backward  8192 x 4096         V = 2, 4, 8: 96, 72, 63
 //             32768 x 1280 bf16   V = 1, 4, 5, 8: 232, 76, 61, 80
@@ -523,19 +523,27 @@ inline bool row_shape(const RowWant& q, RowShape* best) {
   return least >= 0.0;
 }
 
-// One row a team of up to kMaxRowT threads and V chunks: 1, 2 or 4, the
-// narrowest slices that hold the row.
-inline bool single_row_shape(int64_t n, RowShape* r) {
+// One row a team of up to kMaxRowT threads and V chunks, no ring. Up to 3 rows an
+// SM the shortest chain counts: the narrowest slices that hold the row. More rows
+// (single elements alone come here): what counts is how many fit on an SM, so the
+// fewest registers, T (V + 2). us, fp32 to bf16, by V = 1, 2, 4:
+//   300 x 1001 3.3, 3.5, 3.8; 1031 x 1001 6.0, 6.1, 4.6; 1031 x 1501 7.8, 6.4, 6.9
+//   300 x 4001 -, 6.2, 5.2; 1031 x 4001 -, 13.4, 10.9
+// (V = 8 spills: 1031 x 5003 17.7 instead of 13.2.)
+inline bool single_row_shape(int64_t tokens, int64_t n, RowShape* r) {
   const int64_t chunks = (n + kChunk - 1) / kChunk;
+  int64_t least = 0;
   for (int v : {1, 2, 4}) {
     const int64_t t = (chunks + 32 * v - 1) / (32 * v) * 32;
     if (t > (v == 4 ? kMaxRowT : kMaxRowT / 2)) continue;
+    const int64_t cost = t * (v + 2);
+    if (least > 0 && (tokens <= 3 * kSms || cost >= least)) continue;
+    least = cost;
     r->T = static_cast<int>(t);
     r->V = v;
     r->teams = std::max(1, 128 / r->T);
-    return true;
   }
-  return false;
+  return least > 0;
 }
 
 // Lets a kernel take the ring's share of shared memory; asked for once per
