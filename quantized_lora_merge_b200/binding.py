@@ -591,22 +591,24 @@ def _here(jobs, *others) -> None:
         index = jobs.device_index
     else:
         index = _device_index(jobs) if len(jobs) else None
-    found = set() if index is None else {index}
     for t in others:
         if t is None:
             continue
-        if t.device.type != "cuda" or not t.is_contiguous():
-            raise ValueError("workspace and norm must be contiguous and on a CUDA device, got "
-                             f"{t.device}")
-        found.add(t.device.index)
-    if found and found != {torch.cuda.current_device()}:
-        raise ValueError(f"tensors are on cuda:{', cuda:'.join(map(str, sorted(found)))}, the "
-                         f"current device is cuda:{torch.cuda.current_device()}")
+        at = t.get_device()
+        if at < 0 or not t.is_contiguous():
+            raise ValueError("workspace and norm must be contiguous and on a CUDA device")
+        if index is None:
+            index = at
+        elif at != index:
+            raise ValueError(f"workspace or norm is on cuda:{at}, other tensors on cuda:{index}")
+    if index is not None and index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
 
 
 def _norm_scalar(norm) -> int:
     import torch
-    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device.type != "cuda":
+    if norm.dtype != torch.float32 or norm.numel() != 1 or not norm.is_cuda:
         raise TypeError("norm must be one fp32 element on a CUDA device")
     return norm.data_ptr()
 

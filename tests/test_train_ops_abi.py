@@ -192,6 +192,9 @@ def test_binding_refuses_workspaces_and_norms_elsewhere(monkeypatch):
         def __init__(self, device, contiguous=True):
             self.device, self.contiguous = torch.device(device), contiguous
 
+        def get_device(self):
+            return -1 if self.device.index is None else self.device.index
+
         def is_contiguous(self):
             return self.contiguous
 
@@ -202,7 +205,7 @@ def test_binding_refuses_workspaces_and_norms_elsewhere(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     B._here([Job()], On("cuda:0"), None)
     B._here([], None)
-    for jobs, other, needle in (([Job()], On("cpu"), "CUDA"), ([Job()], On("cuda:1"), "cuda:0, cuda:1"),
+    for jobs, other, needle in (([Job()], On("cpu"), "CUDA"), ([Job()], On("cuda:1"), "on cuda:1, other tensors on cuda:0"),
                                 ([], On("cuda:1"), "cuda:1"), ([Job()], On("cuda:0", False), "contiguous")):
         with pytest.raises(ValueError, match=needle):
             B._here(jobs, other)
