@@ -82,6 +82,17 @@ def test_norm_and_clipping(counts, dtypes, shift):
         assert bool((buf[:at] == GUARD).all()) and bool((buf[at + t.numel():] == GUARD).all())
 
 
+@pytest.mark.parametrize("tensors", [63, 64, 65, 255, 256, 257, 511, 512, 513])
+def test_tables_of_every_size(tensors):
+    counts = [1 + 37 * k % 501 for k in range(tensors)]
+    ts = [t for _, t, _ in _tensors(counts, [F32, BF16], seed=tensors)]
+    before = [t.clone() for t in ts]
+    want = math.sqrt(sum(float((t.double() ** 2).sum()) for t in ts))
+    assert _norm(ts) == pytest.approx(want, rel=R.NORM_RTOL)
+    assert _clip(ts, 1.0) == pytest.approx(want, rel=R.NORM_RTOL)
+    _check_clipped(before, ts, want, 1.0)
+
+
 @pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-20, 1e18, 1e25, 1e36])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_values_whose_squares_leave_fp32(scale, dtype):
