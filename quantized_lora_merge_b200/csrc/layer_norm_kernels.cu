@@ -136,13 +136,23 @@ __global__ void __launch_bounds__(kBlock, 1)
 // shared memory. What counts for a few rows is the depth of dependent loads: one.
 // Single elements take this way for more rows too, and there the parameters come
 // after the sums, from L1: 48 registers instead of 64 let four rows of 5003 columns
-// share an SM instead of three (1031 x 5003: 13.1 -> 11.2 us).
+// share an SM instead of three (1031 x 5003: 13.1 -> 11.2 us). Bound there by
+// instructions, 51 an element at 0.67 a cycle with types at run time; with fp32 or
+// not at compile time 9.0 us.
 template <typename F>
 constexpr int kRowRegisters = F::V == 1 ? 32 : F::V == 2 ? (F::VEC ? 56 : 40) : F::V == 4 && !F::VEC ? 48 : 64;
-template <typename F>
+// An element type that is fp32 or not at compile time (T32), or known at run time
+// only (kAnyType); 16-bit types select between the conversions.
+constexpr int kAnyType = -1;
+template <int T32>
+__device__ __forceinline__ int known_type(int type) {
+  return T32 == kAnyType ? type : T32 == 1 ? static_cast<int>(kF32) : type == kF16 ? static_cast<int>(kF16) : static_cast<int>(kBf16);
+}
+template <typename F, int X32, int P32, int Y32>
 __global__ void __maxnreg__(kRowRegisters<F>)
     layer_norm_row_kernel(const __grid_constant__ LayerNormJob j, const __grid_constant__ RowShape r) {
   __shared__ float scratch[2 * 32];
+  const int x_type = known_type<X32>(j.x_type), p_type = known_type<P32>(j.param_type), y_type = known_type<Y32>(j.y_type);
   constexpr bool kLate = F::V > 1 && !F::VEC;
   const int T = r.T, team = threadIdx.x / T, t = threadIdx.x - team * T;
   const int n = static_cast<int>(j.n);
@@ -151,13 +161,13 @@ __global__ void __maxnreg__(kRowRegisters<F>)
   if (T > 32 && !live) return;
   const Columns<F> c(t, live ? n : 0);
   RawRow<F> rx, rw, rb;
-  rx.load(row_ptr(j.x, live ? row : 0, j.ld_x, j.x_type), j.x_type, c);
+  rx.load(row_ptr(j.x, live ? row : 0, j.ld_x, x_type), x_type, c);
   if (!kLate) {
-    rw.load(j.weight, j.param_type, c);
-    rb.load(j.bias, j.param_type, c);
+    rw.load(j.weight, p_type, c);
+    rb.load(j.bias, p_type, c);
   }
   F2 x[2 * F::V], p[2 * F::V];
-  rx.convert(j.x_type, x);
+  rx.convert(x_type, x);
   float mean, rstd;
   row_stats<F>(x, c, 1.0f / static_cast<float>(n), j.eps, T, team, scratch, &mean, &rstd);
   if (!live) return;
@@ -169,18 +179,18 @@ __global__ void __maxnreg__(kRowRegisters<F>)
 #pragma unroll
   for (int i = 0; i < 2 * F::V; ++i) x[i] = x[i] * scale;
   if (j.weight != nullptr) {
-    if (kLate) rw.load(j.weight, j.param_type, c);
-    rw.convert(j.param_type, p);
+    if (kLate) rw.load(j.weight, p_type, c);
+    rw.convert(p_type, p);
 #pragma unroll
     for (int i = 0; i < 2 * F::V; ++i) x[i] = x[i] * p[i];
   }
   if (j.bias != nullptr) {
-    if (kLate) rb.load(j.bias, j.param_type, c);
-    rb.convert(j.param_type, p);
+    if (kLate) rb.load(j.bias, p_type, c);
+    rb.convert(p_type, p);
 #pragma unroll
     for (int i = 0; i < 2 * F::V; ++i) x[i] = x[i] + p[i];
   }
-  write_row<F>(static_cast<char*>(row_ptr(j.y, row, j.ld_y, j.y_type)), j.y_type, c, x);
+  write_row<F>(static_cast<char*>(row_ptr(j.y, row, j.ld_y, y_type)), y_type, c, x);
 }
 
 // Rows too wide for registers: a block per row, three walks over it (the later
@@ -254,6 +264,19 @@ cudaError_t fwd_by_v(const LayerNormJob& j, const RowShape& r, bool vec, unsigne
   }
   return cudaErrorInvalidConfiguration;
 }
+template <bool VEC, int X32, int P32, int Y32>
+void launch_rows(const LayerNormJob& j, const RowShape& r, unsigned grid, int threads, cudaStream_t s) {
+  if (r.V == 1) layer_norm_row_kernel<Form<1, VEC>, X32, P32, Y32><<<grid, threads, 0, s>>>(j, r);
+  else if (r.V == 2) layer_norm_row_kernel<Form<2, VEC>, X32, P32, Y32><<<grid, threads, 0, s>>>(j, r);
+  else layer_norm_row_kernel<Form<4, VEC>, X32, P32, Y32><<<grid, threads, 0, s>>>(j, r);
+}
+template <int X32>
+void rows_by_type(const LayerNormJob& j, const RowShape& r, bool p32, bool y32, unsigned grid, int threads, cudaStream_t s) {
+  if (p32 && y32) launch_rows<false, X32, 1, 1>(j, r, grid, threads, s);
+  else if (p32) launch_rows<false, X32, 1, 0>(j, r, grid, threads, s);
+  else if (y32) launch_rows<false, X32, 0, 1>(j, r, grid, threads, s);
+  else launch_rows<false, X32, 0, 0>(j, r, grid, threads, s);
+}
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormJob& j, cudaStream_t s) {
@@ -261,23 +284,16 @@ cudaError_t launch_layer_norm(const LayerNormJob& j, cudaStream_t s) {
                    reinterpret_cast<uintptr_t>(j.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(j.bias) % 16 == 0;
   RowShape r;
   // Few rows: no ring. Single elements leave the ring a smaller lead: 1031 x 5003
-  // takes 11.2 us this way and 18.7 with it.
+  // takes 9.0 us this way and 18.7 with it.
   if (j.tokens <= (vec ? 1 : 8) * kSms && single_row_shape(j.tokens, j.n, &r)) {
     const unsigned grid = static_cast<unsigned>((j.tokens + r.teams - 1) / r.teams);
     const int threads = r.threads();
-    switch (r.V) {
-      case 1:
-        if (vec) layer_norm_row_kernel<Form<1, true>><<<grid, threads, 0, s>>>(j, r);
-        else layer_norm_row_kernel<Form<1, false>><<<grid, threads, 0, s>>>(j, r);
-        break;
-      case 2:
-        if (vec) layer_norm_row_kernel<Form<2, true>><<<grid, threads, 0, s>>>(j, r);
-        else layer_norm_row_kernel<Form<2, false>><<<grid, threads, 0, s>>>(j, r);
-        break;
-      default:
-        if (vec) layer_norm_row_kernel<Form<4, true>><<<grid, threads, 0, s>>>(j, r);
-        else layer_norm_row_kernel<Form<4, false>><<<grid, threads, 0, s>>>(j, r);
-        break;
+    if (vec) {                                 // up to a row an SM: types at run time
+      launch_rows<true, kAnyType, kAnyType, kAnyType>(j, r, grid, threads, s);
+    } else {
+      const bool p32 = j.param_type == kF32, y32 = j.y_type == kF32;
+      if (j.x_type == kF32) rows_by_type<1>(j, r, p32, y32, grid, threads, s);
+      else rows_by_type<0>(j, r, p32, y32, grid, threads, s);
     }
     return counted(cudaGetLastError());
   }

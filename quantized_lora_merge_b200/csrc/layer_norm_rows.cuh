@@ -526,10 +526,10 @@ inline bool row_shape(const RowWant& q, RowShape* best) {
 // One row a team of up to kMaxRowT threads and V chunks, no ring. Up to 3 rows an
 // SM the shortest chain counts: the narrowest slices that hold the row. More rows
 // (single elements alone come here): what counts is how many fit on an SM, so the
-// fewest registers, T (V + 2). us, fp32 to bf16, by V = 1, 2, 4:
+// fewest registers, T (V + 2). us by V = 1, 2, 4 (with types at run time):
 //   300 x 1001 3.3, 3.5, 3.8; 1031 x 1001 6.0, 6.1, 4.6; 1031 x 1501 7.8, 6.4, 6.9
 //   300 x 4001 -, 6.2, 5.2; 1031 x 4001 -, 13.4, 10.9
-// (V = 8 spills: 1031 x 5003 17.7 instead of 13.2.)
+// (V = 8 spills: 1031 x 5003 fp32 17.7 instead of 13.2.)
 inline bool single_row_shape(int64_t tokens, int64_t n, RowShape* r) {
   const int64_t chunks = (n + kChunk - 1) / kChunk;
   int64_t least = 0;
