@@ -64,6 +64,7 @@ __device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c
 template <int TX, typename F>
 __global__ void __launch_bounds__(kBlock, 1)
     layer_norm_kernel(const __grid_constant__ LayerNormJob j, const __grid_constant__ RowShape r) {
+  static_assert(F::VEC, "single elements do not go through the ring");
   char* ring = smem();
   __shared__ float scratch[2 * 32];
   const int T = r.T, team = threadIdx.x / T, t = threadIdx.x - team * T;
@@ -80,7 +81,6 @@ __global__ void __launch_bounds__(kBlock, 1)
   const int64_t ahead = step * (r.stages - 1);
   const int64_t x_step = step * j.ld_x * elem_bytes(j.x_type), y_step = step * j.ld_y * elem_bytes(j.y_type);
   const char* next = static_cast<const char*>(row_ptr(j.x, row, j.ld_x, j.x_type));
-  const char* here = next;
   char* y = static_cast<char*>(row_ptr(j.y, row, j.ld_y, j.y_type));
   const auto fetch = [&](int slot, int64_t which) {
     if (which < j.tokens && !idle) fetch_row<kBytes<TX>, F>(mine + slot * r.stage_bytes, next, j.x, n, t, T);
@@ -88,7 +88,6 @@ __global__ void __launch_bounds__(kBlock, 1)
     next += x_step;
   };
   clear_tails(ring, r.teams * r.stages, r.stage_bytes, n * elem_bytes(j.x_type) / 16 * 16, r.stage_bytes);
-  if (!F::VEC) __syncthreads();                   // copies write there too, later
   for (int s = 0; s + 1 < r.stages; ++s) fetch(s, row + s * step);
   stage_params<F::VEC>(weight, j.weight, j.param_type, n, width, 1.0f);
   stage_params<F::VEC>(bias, j.bias, j.param_type, n, width, 0.0f);
@@ -96,14 +95,14 @@ __global__ void __launch_bounds__(kBlock, 1)
   if (T > 32 && idle) return;
   int slot = 0;
   // threads of one warp leave together: the block's first team decides
-  for (int64_t base = row - team; base < j.tokens; base += step, row += step, here += x_step, y += y_step) {
+  for (int64_t base = row - team; base < j.tokens; base += step, row += step, y += y_step) {
     const bool live = row < j.tokens && !idle;
     fetch(slot == 0 ? r.stages - 1 : slot - 1, row + ahead);
     copy_wait(r.stages - 1);
     arrive_sync<F::VEC>(T, team);
     F2 x[2 * F::V];
     if (live) {
-      const uint32_t stage = mine + slot * r.stage_bytes + (F::VEC ? 0 : granule_shift(here));
+      const uint32_t stage = mine + slot * r.stage_bytes;
 #pragma unroll
       for (int k = 0; k < F::V; ++k) read_chunk<TX, F>(stage, j.x_type, c, k, x[2 * k], x[2 * k + 1]);
     } else {
@@ -132,13 +131,13 @@ __global__ void __launch_bounds__(kBlock, 1)
   }
 }
 
-// One row a team and few rows: straight from memory, no ring, no parameters in
-// shared memory. What counts for a few rows is the depth of dependent loads: one.
-// Single elements take this way for more rows too, and there the parameters come
-// after the sums, from L1: 48 registers instead of 64 let four rows of 5003 columns
-// share an SM instead of three (1031 x 5003: 13.1 -> 11.2 us). Bound there by
-// instructions, 51 an element at 0.67 a cycle with types at run time; with fp32 or
-// not at compile time 9.0 us.
+// One row a team: straight from memory, no ring, no parameters in shared memory.
+// What counts for a few rows is the depth of dependent loads: one. Single elements
+// take this way for any number of rows, and there the parameters come after the
+// sums, from L1: 48 registers instead of 64 let four rows of 5003 columns share an
+// SM instead of three (1031 x 5003: 13.1 -> 11.2 us). Bound there by instructions,
+// 51 an element at 0.67 a cycle with types at run time; with fp32 or not at compile
+// time 9.0 us.
 template <typename F>
 constexpr int kRowRegisters = F::V == 1 ? 32 : F::V == 2 ? (F::VEC ? 56 : 40) : F::V == 4 && !F::VEC ? 48 : 64;
 // An element type that is fp32 or not at compile time (T32), or known at run time
@@ -234,7 +233,7 @@ cudaError_t launch_fwd(const LayerNormJob& j, const RowShape& r, unsigned grid, 
 }
 // The V of row_shape.
 template <int TX>
-cudaError_t fwd_by_v(const LayerNormJob& j, const RowShape& r, bool vec, unsigned grid, size_t smem, cudaStream_t s) {
+cudaError_t fwd_by_v(const LayerNormJob& j, const RowShape& r, unsigned grid, size_t smem, cudaStream_t s) {
   if (r.L == 16) {
     switch (r.V) {
       case 2: return launch_fwd<TX, Form<2, true, 16>>(j, r, grid, smem, s);
@@ -246,7 +245,7 @@ cudaError_t fwd_by_v(const LayerNormJob& j, const RowShape& r, bool vec, unsigne
     }
     return cudaErrorInvalidConfiguration;
   }
-  switch (vec ? r.V : -r.V) {
+  switch (r.V) {
     case 1: return launch_fwd<TX, Form<1, true>>(j, r, grid, smem, s);
     case 2: return launch_fwd<TX, Form<2, true>>(j, r, grid, smem, s);
     case 3: return launch_fwd<TX, Form<3, true>>(j, r, grid, smem, s);
@@ -257,10 +256,6 @@ cudaError_t fwd_by_v(const LayerNormJob& j, const RowShape& r, bool vec, unsigne
     case 10: return launch_fwd<TX, Form<10, true>>(j, r, grid, smem, s);
     case 12: return launch_fwd<TX, Form<12, true>>(j, r, grid, smem, s);
     case 16: return launch_fwd<TX, Form<16, true>>(j, r, grid, smem, s);
-    case -1: return launch_fwd<TX, Form<1, false>>(j, r, grid, smem, s);
-    case -2: return launch_fwd<TX, Form<2, false>>(j, r, grid, smem, s);
-    case -4: return launch_fwd<TX, Form<4, false>>(j, r, grid, smem, s);
-    case -8: return launch_fwd<TX, Form<8, false>>(j, r, grid, smem, s);
   }
   return cudaErrorInvalidConfiguration;
 }
@@ -283,12 +278,16 @@ cudaError_t launch_layer_norm(const LayerNormJob& j, cudaStream_t s) {
   const bool vec = rows_aligned(j.x, j.ld_x, j.n, j.x_type) && rows_aligned(j.y, j.ld_y, j.n, j.y_type) &&
                    reinterpret_cast<uintptr_t>(j.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(j.bias) % 16 == 0;
   RowShape r;
-  // Few rows: no ring. Single elements leave the ring a smaller lead: 1031 x 5003
-  // takes 9.0 us this way and 18.7 with it.
-  if (j.tokens <= (vec ? 1 : 8) * kSms && single_row_shape(j.tokens, j.n, &r)) {
+  // Without the ring: few rows, and single elements, for which the ring's copies
+  // and barriers cost more than its lead is worth. us without and with it:
+  //   single elements  1031 x 5003 9.0, 18.7; 2000 x 1001 5.6, 7.1; 8192 x 1001
+  //                    20.4, 19.5; 8192 x 4097 53, 72
+  //   chunks           200 x 320 2.3, 3.1; 200 x 4096 3.9, 5.1; 300 x 4096 5.6, 5.2;
+  //                    600 x 1280 4.2, 3.7
+  if ((!vec || j.tokens <= 2 * kSms) && single_row_shape(j.tokens, j.n, &r)) {
     const unsigned grid = static_cast<unsigned>((j.tokens + r.teams - 1) / r.teams);
     const int threads = r.threads();
-    if (vec) {                                 // up to a row an SM: types at run time
+    if (vec) {                                 // up to two rows an SM: types at run time
       launch_rows<true, kAnyType, kAnyType, kAnyType>(j, r, grid, threads, s);
     } else {
       const bool p32 = j.param_type == kF32, y32 = j.y_type == kF32;
@@ -297,15 +296,15 @@ cudaError_t launch_layer_norm(const LayerNormJob& j, cudaStream_t s) {
     }
     return counted(cudaGetLastError());
   }
-  if (!row_shape(RowWant{j.tokens, j.n, vec, kFwdMaxV, j.x_type, -1, 2}, &r)) {
+  if (!vec || !row_shape(RowWant{j.tokens, j.n, true, kFwdMaxV, j.x_type, -1, 2}, &r)) {
     layer_norm_wide_kernel<<<grid_of(j.tokens, 1 << 20), kWideThreads, 0, s>>>(j);
     return counted(cudaGetLastError());
   }
   const unsigned grid = grid_of((j.tokens + r.teams - 1) / r.teams, kSms);
   const size_t smem = static_cast<size_t>(r.params) + 2 * static_cast<size_t>(slot_columns(r)) * sizeof(float);
-  if (j.x_type == kF32) return fwd_by_v<kF32>(j, r, vec, grid, smem, s);
-  if (j.x_type == kBf16) return fwd_by_v<kBf16>(j, r, vec, grid, smem, s);
-  return fwd_by_v<kF16>(j, r, vec, grid, smem, s);
+  if (j.x_type == kF32) return fwd_by_v<kF32>(j, r, grid, smem, s);
+  if (j.x_type == kBf16) return fwd_by_v<kBf16>(j, r, grid, smem, s);
+  return fwd_by_v<kF16>(j, r, grid, smem, s);
 }
 
 }  // namespace intlora

@@ -18,11 +18,12 @@
 // Two ways through the ring:
 //   VEC   rows start at 16-byte boundaries and fill whole 16-byte granules: a
 //         warp copies its own columns; a thread works on chunks of 4 of them
-//   else  the team copies the row's granules, wherever the row starts in the
-//         first one, and a thread works on single columns, 32 apart. A granule
-//         that begins before the tensor is fetched element by element and one
-//         that ends behind the row is cut short: nothing outside [first
-//         element, last element] of the tensor is read.
+//   else  (gradients alone; the forward needs no ring for such rows) the team
+//         copies the row's granules, wherever the row starts in the first one, and
+//         a thread works on single columns, 32 apart. A granule that begins before
+//         the tensor is fetched element by element and one that ends behind the
+//         row is cut short: nothing outside [first element, last element] of the
+//         tensor is read.
 #pragma once
 
 #include <algorithm>
@@ -503,7 +504,7 @@ inline bool row_shape(const RowWant& q, RowShape* best) {
   for (int lanes : {32, 16}) {
     for (int v : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
       if (v > q.max_v || (lanes == 16 && (!q.vec || v > 8 || 16 * v < chunks))) continue;
-      if (!q.vec && v != 1 && v != 2 && v != 4 && v != 8 && !(v == 6 && q.second_type >= 0)) continue;
+      if (!q.vec && v != 1 && v != 2 && v != 4 && v != 6 && v != 8) continue;
       RowShape r;
       const int64_t t = lanes == 16 ? 16 : (chunks + 32 * v - 1) / (32 * v) * 32;
       if (t > kBlock) continue;
