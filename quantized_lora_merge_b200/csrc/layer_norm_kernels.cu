@@ -16,10 +16,83 @@ namespace {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// Mean and rstd of a row held in registers; x becomes x - mean.
+// Whether a row's spread may be nothing but the error of its mean: a mean of
+// `steps` roundings is off by up to steps x 2^-24 of it, and the row of equal
+// values c, whose spread is zero, shows |c - mean| as its spread. Rows in registers
+// (17 additions in a thread, 5 across a warp, 32 across warps, the factor 1 / n):
+// standard deviations below 2^-18 of the mean.
+constexpr float kRowSteps = 64.0f;
+__device__ __forceinline__ bool spread_in_doubt(float mean, float var, float steps) {
+  const float off = steps * 0x1p-24f * mean;
+  return mean != 0.0f && var <= off * off;
+}
+
+// Mean and variance of a row in doubt, formed again about a corrected mean. What
+// a row of equal values has left over its mean is exact and has few bits, so the
+// sums of that are exact, and so are their quotients by n (not by a rounded 1 / n):
+// it ends at its value and at the variance zero. Teams of one warp come here
+// together; those not in doubt keep what they have. `less` is what the row less
+// its old mean is to be reduced by.
+struct Moments {
+  float mean, var, less;
+};
+__device__ __noinline__ Moments settle_row(const void* row, int type, int64_t count, float n, int t, int T, int team,
+                                           float* scratch, bool doubt, float mean, float var) {
+  float s[1] = {0.0f}, s2[2] = {0.0f, 0.0f};
+  for (int64_t c = t; c < count; c += T) s[0] += load_elem(row, c, type) - mean;
+  team_sum<1>(s, T, team, scratch);
+  const float better = mean + s[0] / n;
+  for (int64_t c = t; c < count; c += T) {
+    const float v = load_elem(row, c, type) - better;
+    s2[0] += v;
+    s2[1] = fmaf(v, v, s2[1]);
+  }
+  team_sum<2>(s2, T, team, scratch + 32);
+  if (!doubt) return Moments{mean, var, 0.0f};
+  const float rest = s2[0] / n;                // what the better mean has lost to rounding
+  return Moments{better + rest, fmaxf(fmaf(-rest, rest, s2[1] / n), 0.0f), (better - mean) + rest};
+}
+
+// A row in doubt, from its elements on: x is still what it was, in shared memory
+// or, where the row is not written yet, in memory. Parameters: fp32 in shared
+// memory, or those of the job (weight == nullptr). For such rows alone, at the row's
+// end and out of line, where little is live. us: 8192 x 4096 bf16 28.6, fp32 36.3 (in
+// line behind the sums 32.1 and 36.7, all rows corrected there 30.1 and 43.3,
+// nothing corrected 28.6 and 36.1); what is left is the test of every row: 16384 x
+// 320 fp16 6.96 (6.72 without), 30000 x 40 fp32 7.4 (7.0).
+__device__ __noinline__ void redo_row(const LayerNormJob& j, const void* x, int64_t row, int count, const float* weight,
+                                      const float* bias, int t, int T, int team, float* scratch, bool doubt, float mean,
+                                      float var) {
+  team_sync(T, team);                          // what the team wrote comes before what it writes here
+  const Moments m = settle_row(x, j.x_type, count, static_cast<float>(j.n), t, T, team, scratch, doubt, mean, var);
+  if (doubt) {
+    const float rstd = rsqrtf(m.var + j.eps);
+    if (t == 0) {
+      if (j.mean != nullptr) j.mean[row] = m.mean;
+      if (j.rstd != nullptr) j.rstd[row] = rstd;
+    }
+    void* y = row_ptr(j.y, row, j.ld_y, j.y_type);
+    for (int c = t; c < count; c += T) {
+      float o = ((load_elem(x, c, j.x_type) - mean) - m.less) * rstd;
+      if (weight != nullptr) {
+        o = fmaf(o, weight[c], bias[c]);
+      } else {
+        if (j.weight != nullptr) o *= load_elem(j.weight, c, j.param_type);
+        if (j.bias != nullptr) o += load_elem(j.bias, c, j.param_type);
+      }
+      store_elem(y, c, j.y_type, o);
+    }
+  }
+  team_sync(T, team);                          // the row's place may be taken
+}
+
+// Mean and variance of a row held in registers; x becomes x - mean. scratch: five
+// parts of 32, of which the last three are redo_row's, so that no barrier stands
+// between the reads of one sum and the writes of the next.
+constexpr int kScratch = 5 * 32;
 template <typename F>
-__device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c, float inv_n, float eps, int T,
-                                          int team, float* scratch, float* mean_out, float* rstd_out) {
+__device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c, float inv_n, int T, int team,
+                                          float* scratch, float* mean_out, float* var_out) {
   F2 a = x[0], b = x[1];
 #pragma unroll
   for (int k = 1; k < F::V; ++k) {
@@ -58,7 +131,7 @@ __device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c
   s[0] = both(a + b);
   team_sum<1>(s, T, team, scratch + 32);       // another part: no barrier between the reads and these writes
   *mean_out = mean;
-  *rstd_out = rsqrtf(s[0] * inv_n + eps);      // within 2 units in the last place
+  *var_out = s[0] * inv_n;
 }
 
 template <int TX, typename F>
@@ -66,7 +139,7 @@ __global__ void __launch_bounds__(kBlock, 1)
     layer_norm_kernel(const __grid_constant__ LayerNormJob j, const __grid_constant__ RowShape r) {
   static_assert(F::VEC, "single elements do not go through the ring");
   char* ring = smem();
-  __shared__ float scratch[2 * 32];
+  __shared__ float scratch[kScratch];
   const int T = r.T, team = threadIdx.x / T, t = threadIdx.x - team * T;
   const int n = static_cast<int>(j.n);
   const float inv_n = 1.0f / static_cast<float>(n);
@@ -101,8 +174,8 @@ __global__ void __launch_bounds__(kBlock, 1)
     copy_wait(r.stages - 1);
     arrive_sync<F::VEC>(T, team);
     F2 x[2 * F::V];
+    const uint32_t stage = mine + slot * r.stage_bytes;
     if (live) {
-      const uint32_t stage = mine + slot * r.stage_bytes;
 #pragma unroll
       for (int k = 0; k < F::V; ++k) read_chunk<TX, F>(stage, j.x_type, c, k, x[2 * k], x[2 * k + 1]);
     } else {
@@ -110,24 +183,29 @@ __global__ void __launch_bounds__(kBlock, 1)
       for (int i = 0; i < 2 * F::V; ++i) x[i] = f2(0.0f);
     }
     slot = slot + 1 == r.stages ? 0 : slot + 1;
-    float mean, rstd;
-    row_stats<F>(x, c, inv_n, j.eps, T, team, scratch, &mean, &rstd);
+    float mean, var;
+    row_stats<F>(x, c, inv_n, T, team, scratch, &mean, &var);
+    const bool doubt = spread_in_doubt(mean, var, kRowSteps);
     if (T <= 32) __syncwarp();                 // every lane has read the slot that the next copy may take
-    if (!live) continue;
-    if (t == 0) {
-      if (j.mean != nullptr) j.mean[row] = mean;
-      if (j.rstd != nullptr) j.rstd[row] = rstd;
-    }
-    const F2 scale = f2(rstd);
+    if (live) {
+      const float rstd = rsqrtf(var + j.eps);  // within 2 units in the last place
+      if (t == 0) {
+        if (j.mean != nullptr) j.mean[row] = mean;
+        if (j.rstd != nullptr) j.rstd[row] = rstd;
+      }
+      const F2 scale = f2(rstd);
 #pragma unroll
-    for (int k = 0; k < F::V; ++k) {
-      F2 wa, wb, ba, bb;
-      param_chunk<F>(r.params, c, k, wa, wb);
-      param_chunk<F>(r.params + width * 4, c, k, ba, bb);
-      x[2 * k] = fma2(x[2 * k] * scale, wa, ba);
-      x[2 * k + 1] = fma2(x[2 * k + 1] * scale, wb, bb);
+      for (int k = 0; k < F::V; ++k) {
+        F2 wa, wb, ba, bb;
+        param_chunk<F>(r.params, c, k, wa, wb);
+        param_chunk<F>(r.params + width * 4, c, k, ba, bb);
+        x[2 * k] = fma2(x[2 * k] * scale, wa, ba);
+        x[2 * k + 1] = fma2(x[2 * k + 1] * scale, wb, bb);
+      }
+      write_row<F>(y, j.y_type, c, x);
     }
-    write_row<F>(y, j.y_type, c, x);
+    if (__any_sync(0xffffffffu, doubt))
+      redo_row(j, ring + stage, row, live ? n : 0, weight, bias, t, T, team, scratch + 64, doubt, mean, var);
   }
 }
 
@@ -137,9 +215,10 @@ __global__ void __launch_bounds__(kBlock, 1)
 // sums, from L1: 48 registers instead of 64 let four rows of 5003 columns share an
 // SM instead of three (1031 x 5003: 13.1 -> 11.2 us). Bound there by instructions,
 // 51 an element at 0.67 a cycle with types at run time; with fp32 or not at compile
-// time 9.0 us.
+// time 9.0 us, 9.2 with the settling of rows in doubt. (V = 1: 40 registers, since 32
+// spill around the call: 300 x 1001 3.4 us instead of 3.05.)
 template <typename F>
-constexpr int kRowRegisters = F::V == 1 ? 32 : F::V == 2 ? (F::VEC ? 56 : 40) : F::V == 4 && !F::VEC ? 48 : 64;
+constexpr int kRowRegisters = F::V == 1 ? 40 : F::V == 2 ? (F::VEC ? 56 : 40) : F::V == 4 && !F::VEC ? 48 : 64;
 // An element type that is fp32 or not at compile time (T32), or known at run time
 // only (kAnyType); 16-bit types select between the conversions.
 constexpr int kAnyType = -1;
@@ -150,7 +229,7 @@ __device__ __forceinline__ int known_type(int type) {
 template <typename F, int X32, int P32, int Y32>
 __global__ void __maxnreg__(kRowRegisters<F>)
     layer_norm_row_kernel(const __grid_constant__ LayerNormJob j, const __grid_constant__ RowShape r) {
-  __shared__ float scratch[2 * 32];
+  __shared__ float scratch[kScratch];
   const int x_type = known_type<X32>(j.x_type), p_type = known_type<P32>(j.param_type), y_type = known_type<Y32>(j.y_type);
   constexpr bool kLate = F::V > 1 && !F::VEC;
   const int T = r.T, team = threadIdx.x / T, t = threadIdx.x - team * T;
@@ -167,10 +246,19 @@ __global__ void __maxnreg__(kRowRegisters<F>)
   }
   F2 x[2 * F::V], p[2 * F::V];
   rx.convert(x_type, x);
-  float mean, rstd;
-  row_stats<F>(x, c, 1.0f / static_cast<float>(n), j.eps, T, team, scratch, &mean, &rstd);
-  if (!live) return;
-  if (t == 0) {
+  float mean, var;
+  row_stats<F>(x, c, 1.0f / static_cast<float>(n), T, team, scratch, &mean, &var);
+  const bool doubt = live && spread_in_doubt(mean, var, kRowSteps);
+  if (kLate && __any_sync(0xffffffffu, doubt)) {
+    const Moments m = settle_row(row_ptr(j.x, live ? row : 0, j.ld_x, x_type), x_type, live ? n : 0, static_cast<float>(n),
+                                 t, T, team, scratch + 64, doubt, mean, var);
+    mean = m.mean;
+    var = m.var;
+#pragma unroll
+    for (int i = 0; i < 2 * F::V; ++i) x[i] = x[i] + f2(-m.less);
+  }
+  const float rstd = rsqrtf(var + j.eps);      // within 2 units in the last place
+  if (live && t == 0) {
     if (j.mean != nullptr) j.mean[row] = mean;
     if (j.rstd != nullptr) j.rstd[row] = rstd;
   }
@@ -189,33 +277,47 @@ __global__ void __maxnreg__(kRowRegisters<F>)
 #pragma unroll
     for (int i = 0; i < 2 * F::V; ++i) x[i] = x[i] + p[i];
   }
-  write_row<F>(static_cast<char*>(row_ptr(j.y, row, j.ld_y, y_type)), y_type, c, x);
+  if (!kLate && __any_sync(0xffffffffu, doubt)) {          // before x is written over, where y is x
+    redo_row(j, row_ptr(j.x, live ? row : 0, j.ld_x, x_type), row, live ? n : 0, nullptr, nullptr, t, T, team,
+             scratch + 64, doubt, mean, var);
+    if (doubt) return;
+  }
+  if (live) write_row<F>(static_cast<char*>(row_ptr(j.y, row, j.ld_y, y_type)), y_type, c, x);
 }
 
 // Rows too wide for registers: a block per row, three walks over it (the later
-// ones served by L1 and L2).
-__global__ void __launch_bounds__(kWideThreads) layer_norm_wide_kernel(const __grid_constant__ LayerNormJob j) {
-  __shared__ float scratch[2][32];
+// ones served by L1 and L2). Two blocks an SM, which takes at most 32 registers
+// (with 36 and one block 600 x 40000 fp32 took 166 us instead of 137).
+__global__ void __launch_bounds__(kWideThreads, 2) layer_norm_wide_kernel(const __grid_constant__ LayerNormJob j) {
+  __shared__ float scratch[kScratch];
+  const float n = static_cast<float>(j.n);
   for (int64_t row = blockIdx.x; row < j.tokens; row += gridDim.x) {
     const void* x = row_ptr(j.x, row, j.ld_x, j.x_type);
     float s[1] = {0.0f};
     for (int64_t c = threadIdx.x; c < j.n; c += kWideThreads) s[0] += load_elem(x, c, j.x_type);
-    team_sum<1>(s, kWideThreads, 0, scratch[0]);
-    const float mean = s[0] / static_cast<float>(j.n);
+    team_sum<1>(s, kWideThreads, 0, scratch);
+    float mean = s[0] / n, less = 0.0f;
     s[0] = 0.0f;
     for (int64_t c = threadIdx.x; c < j.n; c += kWideThreads) {
       const float v = load_elem(x, c, j.x_type) - mean;
       s[0] = fmaf(v, v, s[0]);
     }
-    team_sum<1>(s, kWideThreads, 0, scratch[1]);
-    const float rstd = 1.0f / sqrtf(s[0] / static_cast<float>(j.n) + j.eps);
+    team_sum<1>(s, kWideThreads, 0, scratch + 32);
+    float var = s[0] / n, settled = mean;
+    if (spread_in_doubt(mean, var, kRowSteps + n / kWideThreads)) {
+      const Moments m = settle_row(x, j.x_type, j.n, n, threadIdx.x, kWideThreads, 0, scratch + 64, true, mean, var);
+      settled = m.mean;
+      var = m.var;
+      less = m.less;
+    }
+    const float rstd = 1.0f / sqrtf(var + j.eps);
     if (threadIdx.x == 0) {
-      if (j.mean != nullptr) j.mean[row] = mean;
+      if (j.mean != nullptr) j.mean[row] = settled;
       if (j.rstd != nullptr) j.rstd[row] = rstd;
     }
     void* y = row_ptr(j.y, row, j.ld_y, j.y_type);
     for (int64_t c = threadIdx.x; c < j.n; c += kWideThreads) {
-      float o = (load_elem(x, c, j.x_type) - mean) * rstd;
+      float o = ((load_elem(x, c, j.x_type) - mean) - less) * rstd;
       if (j.weight != nullptr) o *= load_elem(j.weight, c, j.param_type);
       if (j.bias != nullptr) o += load_elem(j.bias, c, j.param_type);
       store_elem(y, c, j.y_type, o);

@@ -290,3 +290,33 @@ def test_gradient_matches_differences_of_the_forward():
         e[i] = h
         diff = (loss(x, w.double() + e) - loss(x, w.double() - e)) / (2 * h)
         assert abs(diff - float(dw[i])) < float(bound[1][i]) + slack + 1e-6
+
+
+# through every form: several rows a warp, half and whole warps, blocks, with and
+# without the ring, chunks and single elements, three walks; widths whose 1/n is
+# no fp32 number
+CONSTANT_ROWS = [(6000, 12), (6000, 40), (1300, 33), (700, 320), (4, 1000), (1300, 1000), (1300, 1001), (1300, 5003),
+                 (300, 12000), (200, 22000), (7, 40000), (7, 40001)]
+
+
+@pytest.mark.parametrize("tokens,n", CONSTANT_ROWS)
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("eps", [1e-5, 1e-12, 0.0])
+def test_constant_rows(tokens, n, dtype, eps):
+    """Their mean is the value itself, whatever 1/n rounds to, and their variance
+    zero: y is the bias, or with eps = 0 what 0 / 0 gives. The rows between them
+    are what they are elsewhere."""
+    values = [3.0, 1000.0, 60000.0, -0.1, 7.3e-3] + ([100000.0, 1e-12, -1e-30, 2.3e25] if dtype != F16 else [])
+    x, w, b, _ = _inputs(tokens, n, dtype, F32, seed=n)
+    rows = torch.arange(tokens, device=dev())
+    constant = rows % 3 != 1
+    x[constant] = torch.tensor(values, device=dev()).to(dtype)[rows[constant] % len(values)][:, None]
+    _, y, mean, rstd = _forward(x, w, b, F32, eps=eps)
+    assert torch.equal(mean[constant], x[constant, 0].float())
+    if eps > 0:
+        assert torch.equal(y[constant], b.expand(int(constant.sum()), n))
+        ref = torch.tensor(eps, device=dev()).double() ** -0.5        # eps travels as fp32
+        assert bool(((rstd[constant].double() / ref - 1).abs() <= 4 * R.U).all())
+    else:
+        assert bool(torch.isnan(y[constant]).all()) and bool(torch.isinf(rstd[constant]).all())
+    _check_forward(x[~constant], w, b, y[~constant], mean[~constant], rstd[~constant], eps=eps)
