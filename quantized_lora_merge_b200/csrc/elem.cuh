@@ -110,7 +110,9 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int type, const float
 // may be set up while the other still runs: it is launched by launch_after, and
 // waits here, before its first access to memory, until the other has ended and
 // its writes are visible. (Launched plainly, the second kernel begins about 1 us
-// later.)
+// later.) What the other has written is read by plain loads: the read-only path
+// (__ldg) is for memory that nothing writes from the kernel's launch on, and such
+// loads need not stay behind this wait.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A&&... args) {

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int i = threadIdx.x; i < nruns * (kRun / 4); i += kJoinThreads) {
     uint4 k = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
     if (i * 4 + 4 <= count) {                  // the lists start at 256-byte boundaries
-      k = __ldg(reinterpret_cast<const uint4*>(key + group) + i);
+      k = *(reinterpret_cast<const uint4*>(key + group) + i);
     } else {
       if (i * 4 < count) k.x = key[group + i * 4];
       if (i * 4 + 1 < count) k.y = key[group + i * 4 + 1];
@@ -338,7 +338,8 @@ struct RawStrip {
       for (int i = 0; i < kWords; ++i) w[k * kWords + i] = 0u;
       if (c >= n) continue;
       if constexpr (!VEC) {
-        w[k] = TYPE == kF32 ? __ldg(static_cast<const uint32_t*>(row) + c) : __ldg(static_cast<const uint16_t*>(row) + c);
+        if constexpr (TYPE == kF32) w[k] = static_cast<const uint32_t*>(row)[c];     // dy, or the chunks' sums
+        else w[k] = __ldg(static_cast<const uint16_t*>(row) + c);
       } else {
         const char* p = static_cast<const char*>(row) + c * elem_bytes(TYPE);
         if constexpr (TYPE == kF32) {
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   Strip<VEC> s;
   s.clear();
   add_rows<TYPE, VEC, TYPE == kF32 && VEC ? 4 : 8>(s, j.dy, j.ld_dy, kChunk, c0, j.n,
-                                                   [&](int64_t i) { return __ldg(pos + a + i); });
+                                                   [&](int64_t i) { return pos[a + i]; });
   float* out = partial + chunk * j.n;
 #pragma unroll
   for (int k = 0; k < Strip<VEC>::C; ++k) {
@@ -751,7 +752,7 @@ __device__ __forceinline__ void add_word(Strip<VEC>& s, const EmbeddingBackwardJ
                                          int64_t from, int64_t to, int64_t c0) {
   add_rows<TYPE, VEC, kRowsAhead<TYPE>>(s, j.dy, j.ld_dy, min(to, w.loose) - from, c0, j.n, [&](int64_t i) {
     const int64_t p = (from + i < w.head ? w.a : w.skip) + from + i;
-    return p - p0 < kPositions ? words.pos[p - p0] : __ldg(pos + p);
+    return p - p0 < kPositions ? words.pos[p - p0] : pos[p];
   });
   const int64_t begin = max(from, w.loose);
   add_rows<kF32, VEC, kRowsAhead<kF32>>(s, partial, j.n, to - begin, c0, j.n,
