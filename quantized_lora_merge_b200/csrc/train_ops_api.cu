@@ -36,7 +36,11 @@ intlora_status fail(intlora_status st, const char* fmt, ...) {
   return st;
 }
 
+// The error is reported here and now: calls that returned it (cudaLaunchKernelEx,
+// cudaFuncSetAttribute) leave it as the runtime's last error too, where the next
+// call's first launch would find it.
 intlora_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   return fail(INTLORA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
