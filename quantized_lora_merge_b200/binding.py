@@ -616,7 +616,9 @@ def _norm_scalar(norm) -> int:
 class Descriptors:
     """A list of descriptors converted to their C structs once, for calls that
     repeat on the same buffers (the per-call conversion of a 128-layer list
-    costs milliseconds of Python). Pass it wherever a list is accepted."""
+    costs milliseconds of Python). Pass it wherever a list is accepted. The
+    structs hold addresses, so the descriptors, and with them their tensors, live
+    as long as this does."""
 
     _STRUCT = {}
 
@@ -630,6 +632,7 @@ class Descriptors:
             if type(it) is not type(items[0]):
                 raise TypeError("mixed descriptor types")
             self.arr[k] = it.to_c()
+        self.items = items
         self.count = len(items)
         self.device_index = _device_index(items) if hasattr(items[0], "device") else None
 
