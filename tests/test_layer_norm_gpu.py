@@ -320,3 +320,18 @@ def test_constant_rows(tokens, n, dtype, eps):
     else:
         assert bool(torch.isnan(y[constant]).all()) and bool(torch.isinf(rstd[constant]).all())
     _check_forward(x[~constant], w, b, y[~constant], mean[~constant], rstd[~constant], eps=eps)
+
+
+@pytest.mark.parametrize("tokens,n", CONSTANT_ROWS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_constant_rows_in_place(tokens, n, dtype):
+    """y in the place of x: the bits of separate tensors, with and without parameters."""
+    x, w, b, _ = _inputs(tokens, n, dtype, F32, seed=n)
+    x[::2] = torch.linspace(-3.0, 70000.0, len(x[::2]), device=dev())[:, None].to(dtype)
+    for weight, bias in ((w, b), (None, b), (w, None)):
+        _, y, mean, rstd = _forward(x, weight, bias, dtype)
+        there = x.clone()
+        B.intlora_layer_norm_batched([B.LayerNormJob(there, weight, bias, there)])
+        assert torch.equal(there, y)
+        assert torch.equal(mean[::2], x[::2, 0].float())
+        assert torch.equal(y[::2], (torch.zeros(n, device=dev()) if bias is None else b).to(dtype).expand_as(y[::2]))
