@@ -479,9 +479,11 @@ intlora_status intlora_train_backward_batched(const intlora_train_backward_job* 
  * Elements are fp32, bf16 or fp16 (INTLORA_TYPE_*), each tensor with a type of
  * its own; arithmetic, statistics and sums are fp32 or wider and every output
  * is rounded once, to nearest, ties to even. Matrices are row-major with a row
- * stride ld in elements (>= n), any alignment of whole elements; rows that start
- * and end at 16-byte boundaries (layer norm) or at multiples of 8 elements
- * (embedding) take wide accesses, others single elements. Results do not depend on the order in which blocks run.
+ * stride ld in elements (>= n), any alignment of whole elements. Wide accesses are
+ * taken where every row of every matrix starts and ends at a 16-byte boundary and
+ * weight and bias start at one (layer norm), or every row starts at a multiple of 8
+ * elements and n is one (embedding); else single elements, two to three times
+ * slower. Results do not depend on the order in which blocks run.
  * tokens, n and vocab < 2^31; every rows * ld at most 2^40.
  * ------------------------------------------------------------------------ */
 #define INTLORA_TYPE_F32 0
@@ -492,7 +494,9 @@ intlora_status intlora_train_backward_batched(const intlora_train_backward_job* 
  * mean = (1/n) sum x, rstd = ((1/n) sum (x - mean)^2 + eps)^-1/2.
  * weight, bias (both param_type, [n]) may be NULL (1 and 0); mean and rstd
  * (fp32 [tokens], what the backward takes) may be NULL. n >= 1, eps finite and
- * >= 0; a constant row with eps = 0 gives what 0 / 0 gives. One launch a job;
+ * >= 0. A row of equal values has that value as its mean and the variance 0,
+ * whatever its sum rounds to: y = bias, or with eps = 0 what 0 / 0 gives. Sums stay
+ * within fp32's range: a row whose sum leaves it gives NaN. One launch a job;
  * the jobs of a call do not depend on one another. y may be x itself (one type
  * and stride); no other overlap of what a job writes with what it reads.
  * Asynchronous on `stream`; no workspace. */
@@ -589,8 +593,10 @@ intlora_status intlora_embedding_backward_batched(const intlora_embedding_backwa
                                                   void* stream);
 
 /* Global norm of many gradient tensors, and clipping by it:
- *   norm = sqrt(sum over all tensors of g^2)      (summed in fp64, stored fp32)
+ *   norm = sqrt(sum over all tensors of g^2)      (stored fp32)
  *   g <- g * min(1, max_norm / (norm + 1e-6))     (in place)
+ * Squares are added 32 at a time in fp32, or in fp64 where fp32's range does not
+ * suffice, and everything beyond in fp64: the norm is within 7 x 2^-24 of itself.
  * The gradients are only read where the factor is 1. A NaN norm makes every
  * gradient NaN, an infinite one makes finite gradients 0: test *norm. Tensors
  * are dense (count elements from g on) and of any number; those that

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kBlock, 1)
 // sums, from L1: 48 registers instead of 64 let four rows of 5003 columns share an
 // SM instead of three (1031 x 5003: 13.1 -> 11.2 us). Bound there by instructions,
 // 51 an element at 0.67 a cycle with types at run time; with fp32 or not at compile
-// time 9.0 us, 9.2 with the settling of rows in doubt. (V = 1: 40 registers, since 32
+// time 38 at 0.61, 9.0 us, or 9.2 with the settling of rows in doubt. (V = 1: 40 registers, since 32
 // spill around the call: 300 x 1001 3.4 us instead of 3.05.)
 template <typename F>
 constexpr int kRowRegisters = F::V == 1 ? 40 : F::V == 2 ? (F::VEC ? 56 : 40) : F::V == 4 && !F::VEC ? 48 : 64;
@@ -381,7 +381,9 @@ cudaError_t launch_layer_norm(const LayerNormJob& j, cudaStream_t s) {
                    reinterpret_cast<uintptr_t>(j.weight) % 16 == 0 && reinterpret_cast<uintptr_t>(j.bias) % 16 == 0;
   RowShape r;
   // Without the ring: few rows, and single elements, for which the ring's copies
-  // and barriers cost more than its lead is worth. us without and with it:
+  // and barriers cost more than its lead is worth, but for narrow rows in their
+  // thousands, where it is 4 % ahead (8192 x 1001): not worth a second form of every
+  // ring kernel. us without and with it:
   //   single elements  1031 x 5003 9.0, 18.7; 2000 x 1001 5.6, 7.1; 8192 x 1001
   //                    20.4, 19.5; 8192 x 4097 53, 72
   //   chunks           200 x 320 2.3, 3.1; 200 x 4096 3.9, 5.1; 300 x 4096 5.6, 5.2;
