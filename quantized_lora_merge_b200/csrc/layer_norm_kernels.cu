@@ -86,13 +86,13 @@ __device__ __noinline__ void redo_row(const LayerNormJob& j, const void* x, int6
   team_sync(T, team);                          // the row's place may be taken
 }
 
-// Mean and variance of a row held in registers; x becomes x - mean. scratch: five
+// Mean, variance and rstd of a row held in registers; x becomes x - mean. scratch: five
 // parts of 32, of which the last three are redo_row's, so that no barrier stands
 // between the reads of one sum and the writes of the next.
 constexpr int kScratch = 5 * 32;
 template <typename F>
-__device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c, float inv_n, int T, int team,
-                                          float* scratch, float* mean_out, float* var_out) {
+__device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c, float inv_n, float eps, int T,
+                                          int team, float* scratch, float* mean_out, float* var_out, float* rstd_out) {
   F2 a = x[0], b = x[1];
 #pragma unroll
   for (int k = 1; k < F::V; ++k) {
@@ -132,6 +132,7 @@ __device__ __forceinline__ void row_stats(F2 (&x)[2 * F::V], const Columns<F>& c
   team_sum<1>(s, T, team, scratch + 32);       // another part: no barrier between the reads and these writes
   *mean_out = mean;
   *var_out = s[0] * inv_n;
+  *rstd_out = rsqrtf(fmaf(s[0], inv_n, eps));  // within 2 units in the last place
 }
 
 template <int TX, typename F>
@@ -183,12 +184,11 @@ __global__ void __launch_bounds__(kBlock, 1)
       for (int i = 0; i < 2 * F::V; ++i) x[i] = f2(0.0f);
     }
     slot = slot + 1 == r.stages ? 0 : slot + 1;
-    float mean, var;
-    row_stats<F>(x, c, inv_n, T, team, scratch, &mean, &var);
+    float mean, var, rstd;
+    row_stats<F>(x, c, inv_n, j.eps, T, team, scratch, &mean, &var, &rstd);
     const bool doubt = spread_in_doubt(mean, var, kRowSteps);
     if (T <= 32) __syncwarp();                 // every lane has read the slot that the next copy may take
     if (live) {
-      const float rstd = rsqrtf(var + j.eps);  // within 2 units in the last place
       if (t == 0) {
         if (j.mean != nullptr) j.mean[row] = mean;
         if (j.rstd != nullptr) j.rstd[row] = rstd;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kBlock, 1)
 // sums, from L1: 48 registers instead of 64 let four rows of 5003 columns share an
 // SM instead of three (1031 x 5003: 13.1 -> 11.2 us). Bound there by instructions,
 // 51 an element at 0.67 a cycle with types at run time; with fp32 or not at compile
-// time 38 at 0.61, 9.0 us, or 9.2 with the settling of rows in doubt. (V = 1: 40 registers, since 32
+// time 38 at 0.61, 9.0 us, or 9.1 with the settling of rows in doubt. (V = 1: 40 registers, since 32
 // spill around the call: 300 x 1001 3.4 us instead of 3.05.)
 template <typename F>
 constexpr int kRowRegisters = F::V == 1 ? 40 : F::V == 2 ? (F::VEC ? 56 : 40) : F::V == 4 && !F::VEC ? 48 : 64;
@@ -246,18 +246,17 @@ __global__ void __maxnreg__(kRowRegisters<F>)
   }
   F2 x[2 * F::V], p[2 * F::V];
   rx.convert(x_type, x);
-  float mean, var;
-  row_stats<F>(x, c, 1.0f / static_cast<float>(n), T, team, scratch, &mean, &var);
+  float mean, var, rstd;
+  row_stats<F>(x, c, 1.0f / static_cast<float>(n), j.eps, T, team, scratch, &mean, &var, &rstd);
   const bool doubt = live && spread_in_doubt(mean, var, kRowSteps);
   if (kLate && __any_sync(0xffffffffu, doubt)) {
     const Moments m = settle_row(row_ptr(j.x, live ? row : 0, j.ld_x, x_type), x_type, live ? n : 0, static_cast<float>(n),
                                  t, T, team, scratch + 64, doubt, mean, var);
     mean = m.mean;
-    var = m.var;
+    if (doubt) rstd = rsqrtf(m.var + j.eps);
 #pragma unroll
     for (int i = 0; i < 2 * F::V; ++i) x[i] = x[i] + f2(-m.less);
   }
-  const float rstd = rsqrtf(var + j.eps);      // within 2 units in the last place
   if (live && t == 0) {
     if (j.mean != nullptr) j.mean[row] = mean;
     if (j.rstd != nullptr) j.rstd[row] = rstd;
